@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define PWQ_ABI_VERSION 5
+#define PWQ_ABI_VERSION 6
 
 typedef enum pwq_status {
     PWQ_OK = 0,
@@ -423,6 +423,70 @@ pwq_status pwq_quantized_matmul_noalloc(const void* X, int x_dtype, int64_t n_to
                                         const uint8_t* packed, const uint16_t* scales, const uint16_t* zeros,
                                         int64_t d_out, int32_t group_size, void* Y, int y_dtype, int64_t ldy,
                                         void* stream);
+
+/* ------------------------------------------------------------------ 8-bit activations
+ * A layer's product in 8-bit integers (W8A8): activations as int8 codes with one float32
+ * scale per token (the symmetric quantizer of [MQM] "Affine Quantization" with Z = 0, taken
+ * over a token's row), multiplied with a layer's codes of up to 8 bits and one scale per
+ * output row (pwq_rtn_quantize / pwq_gptq_quantize_layer with group_size 0, or their _zp
+ * forms).  Per token with values y:
+ *   s    = float32(max |y| / 127); below 2^-120 it counts as 0
+ *   code = nearest integer to y / s, ties to even, so -127 .. 127; s = 0 gives code 0
+ * A token with a value that is not finite gets scale NaN and codes 0, so that its products
+ * come out NaN.  sums[t] = sum of the token's codes, what pwq_quantized_matmul_int8 needs for
+ * the zero-point form.
+ *
+ * pwq_quantize_tokens: y = X, or with channel_scale the float32 quotient X[t][c] /
+ * channel_scale[c] (s_out of pwq_awq_search: "at inference X is divided by s_out").
+ *   X              n_tok x d, x_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldx.
+ *   channel_scale  optional float32[d].
+ *   codes          int8 n_tok x d, leading dimension ldq; scales float32[n_tok].
+ *   sums           optional int32[n_tok].
+ * Codes are those of the exact quotient y / s.  1 <= d <= 65535. */
+pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx,
+                               const float* channel_scale, int8_t* codes, int64_t ldq, float* scales, int32_t* sums,
+                               void* stream);
+
+/* pwq_rms_norm_quantize: the root-mean-square norm ahead of a layer, with the residual's
+ * addition before it and the token quantizer after it:
+ *   h = X + residual, rounded once to x_dtype (h = X without residual)
+ *   y = h * gain / sqrt(mean over the row of h^2 + eps), in float64
+ *   residual  optional n_tok x d of x_dtype, leading dimension ldr.
+ *   gain      optional d values of gain_dtype (any of the three types; NULL: ones).
+ *   eps       >= 0 (a row of zeros with eps 0 is not finite).
+ *   h_out     optional n_tok x d of x_dtype, leading dimension ldh; may be X or residual
+ *             themselves (same pointer and stride), no other outputs may overlap inputs.
+ *             Needs residual.
+ *   codes, scales, sums  as above; codes and scales together, or both NULL (then sums too).
+ *   Y         optional: y itself, rounded to y_dtype, leading dimension ldy (the input of
+ *             pwq_quantized_matmul as float16).  At least one of codes / Y.
+ * 1 <= d <= 65535.  Each value is read and written once; nothing is allocated. */
+pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx, const void* residual,
+                                 int64_t ldr, const void* gain, int gain_dtype, double eps, void* h_out, int64_t ldh,
+                                 int8_t* codes, int64_t ldq, float* scales, int32_t* sums, void* Y, int y_dtype,
+                                 int64_t ldy, void* stream);
+
+/* pwq_quantized_matmul_int8:
+ *   Y[t][o] = x_scales[t] * scales[o] * sum over k of X[t][k] (codes[o][k] - zero[o])
+ * with the sum exact in int32 (zero = 0 and int8 codes without zeros; uint8 codes, zeros
+ * 0 .. 255 and x_sums[t] = sum_k X[t][k] with them).  The result does not depend on how k is
+ * split: it is rounded by the sum's conversion to float32, the two scales and the store.
+ *   X         int8 n_tok x d_in, leading dimension ldx; any int8 values.
+ *   x_scales  float32[n_tok]; x_sums int32[n_tok], required with zeros.
+ *   codes     d_out x d_in, dense, in original column order (act-order layers too: group_size
+ *             0 has one scale per row).
+ *   scales    float16[d_out]; zeros uint16[d_out] or NULL (above 255 taken as 255).
+ *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy.
+ *   ws        pwq_quantized_matmul_int8_workspace_size(n_tok, d_in, d_out) bytes, 16-byte
+ *             aligned (0 bytes: ws may be NULL): the int32 sums of a split k.
+ * Any alignment and sizes with 1 <= d_in <= 65535; rows of X and codes that start at multiples
+ * of 16 bytes (16-byte aligned pointers, ldx and d_in multiples of 16) take the faster kernels.
+ * PWQ_EINVAL when n_tok * d_out needs more tiles of 128 x 128 than one launch holds (2^24). */
+size_t pwq_quantized_matmul_int8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out);
+pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const float* x_scales,
+                                     const int32_t* x_sums, const void* codes, const uint16_t* scales,
+                                     const uint16_t* zeros, int64_t d_out, void* Y, int y_dtype, int64_t ldy, void* ws,
+                                     size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

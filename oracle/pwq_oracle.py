@@ -131,7 +131,8 @@ __all__ = [
     "recon_mse", "recon_mse_trace", "direct_obs", "quantize_layer", "n_groups",
     "storage_bytes", "asym_scale_zero", "quantize_codes_asym", "rtn_asym", "dequant_asym",
     "pack_uint4", "unpack_uint4", "quantized_matmul", "tensor_scales", "channel_abs_mean",
-    "awq_scales", "awq_search",
+    "awq_scales", "awq_search", "quantize_tokens", "rms_norm", "rms_norm_quantize",
+    "quantized_matmul_int8",
 ]
 
 
@@ -647,6 +648,58 @@ def quantized_matmul(X: np.ndarray, codes: np.ndarray, scales: np.ndarray, group
     (and zeros); What exact, the sum over d_in in float64."""
     What = dequant(codes, scales, group_size, g_idx=g_idx, out_dtype=np.float64, zeros=zeros)
     return np.asarray(X, dtype=np.float64) @ What.T
+
+
+# ------------------------------------------------------------------ 8-bit activations
+
+def _token_codes(y: np.ndarray):
+    """(codes, scales, sums) of float64 rows y, one symmetric 8-bit quantizer per row: s =
+    float32(max |y| / 127), 0 below 2^-120; code = nearest(y / s), ties to even; a row that is
+    not finite has scale NaN and codes 0."""
+    T, d = y.shape
+    codes = np.zeros((T, d), dtype=np.int8)
+    scales = np.zeros(T, dtype=np.float32)
+    for t in range(T):
+        if not np.all(np.isfinite(y[t])):
+            scales[t] = np.nan
+            continue
+        s = np.float32(np.max(np.abs(y[t])) / 127.0)
+        if s < np.float32(2.0 ** -120):
+            continue
+        scales[t] = s
+        codes[t] = np.rint(y[t] / np.float64(s)).astype(np.int8)
+    return codes, scales, codes.sum(axis=1, dtype=np.int32)
+
+
+def quantize_tokens(X: np.ndarray, channel_scale: Optional[np.ndarray] = None):
+    """8-bit codes of activations, per token: of X, or of the float32 quotient X / channel_scale."""
+    y = np.asarray(X, dtype=np.float32)
+    if channel_scale is not None:
+        y = y / np.asarray(channel_scale, dtype=np.float32)
+    return _token_codes(y.astype(np.float64))
+
+
+def rms_norm(h: np.ndarray, gain: Optional[np.ndarray], eps: float) -> np.ndarray:
+    """float64 rows h * gain / sqrt(mean(h^2) + eps)."""
+    h = np.asarray(h, dtype=np.float64)
+    y = h / np.sqrt(np.mean(h * h, axis=1, keepdims=True) + eps)
+    return y if gain is None else y * np.asarray(gain, dtype=np.float64)
+
+
+def rms_norm_quantize(h: np.ndarray, gain: Optional[np.ndarray], eps: float):
+    """(codes, scales, sums) of the normed rows."""
+    return _token_codes(rms_norm(h, gain, eps))
+
+
+def quantized_matmul_int8(X: np.ndarray, x_scales: np.ndarray, codes: np.ndarray, scales: np.ndarray,
+                          zeros: Optional[np.ndarray] = None) -> np.ndarray:
+    """float64 x_scales[t] scales[o] sum_k X[t, k] (codes[o, k] - zeros[o]); the sum exact (every
+    product and partial sum is a whole number below 2^53)."""
+    c = np.asarray(codes, dtype=np.float64)
+    if zeros is not None:
+        c = c - np.asarray(zeros, dtype=np.float64).reshape(-1, 1)
+    s = np.asarray(X, dtype=np.float64) @ c.T
+    return s * np.asarray(scales, dtype=np.float64).reshape(1, -1) * np.asarray(x_scales, dtype=np.float64).reshape(-1, 1)
 
 
 # ------------------------------------------------------------------ error measures

@@ -488,4 +488,69 @@ pwq_status pwq_quantized_matmul_noalloc(const void* X, int x_dtype, int64_t n_to
                                    y_dtype, ldy, ws, (hipStream_t)stream));
 }
 
+// ------------------------------------------------------------------ 8-bit activations
+static bool float_dtype(int t) { return t == PWQ_F32 || t == PWQ_F16 || t == PWQ_BF16; }
+static size_t float_size(int t) { return t == PWQ_F32 ? 4 : 2; }
+
+pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx,
+                               const float* channel_scale, int8_t* codes, int64_t ldq, float* scales, int32_t* sums,
+                               void* stream) {
+    if (!float_dtype(x_dtype)) return PWQ_EDTYPE;
+    if (bad_dim(n_tok) || d < 1 || d > TOK_MAX_WIDTH || ldx < d || bad_dim(ldx) || ldq < d || bad_dim(ldq))
+        return PWQ_EINVAL;
+    if (n_tok == 0) return PWQ_OK;
+    if (!X || !codes || !scales || !aligned(X, float_size(x_dtype)) || !aligned(channel_scale, 4) || !aligned(scales, 4) ||
+        !aligned(sums, 4))
+        return PWQ_EINVAL;
+    return hip_status(tok_quant_launch(X, x_dtype, n_tok, d, ldx, channel_scale, codes, ldq, scales, sums,
+                                       (hipStream_t)stream));
+}
+
+pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx, const void* residual,
+                                 int64_t ldr, const void* gain, int gain_dtype, double eps, void* h_out, int64_t ldh,
+                                 int8_t* codes, int64_t ldq, float* scales, int32_t* sums, void* Y, int y_dtype,
+                                 int64_t ldy, void* stream) {
+    if (!float_dtype(x_dtype) || (gain && !float_dtype(gain_dtype)) || (Y && !float_dtype(y_dtype))) return PWQ_EDTYPE;
+    if (bad_dim(n_tok) || d < 1 || d > TOK_MAX_WIDTH || ldx < d || bad_dim(ldx)) return PWQ_EINVAL;
+    if (!(eps >= 0.0) || isinf(eps)) return PWQ_EINVAL;
+    if ((residual && (ldr < d || bad_dim(ldr))) || (h_out && (!residual || ldh < d || bad_dim(ldh))) ||
+        (codes && (ldq < d || bad_dim(ldq))) || (Y && (ldy < d || bad_dim(ldy))))
+        return PWQ_EINVAL;
+    if (n_tok == 0) return PWQ_OK;
+    if (!X || (!codes && !Y) || (codes != nullptr) != (scales != nullptr) || (sums && !codes)) return PWQ_EINVAL;
+    const size_t e = float_size(x_dtype);
+    if (!aligned(X, e) || !aligned(residual, e) || !aligned(h_out, e) || (gain && !aligned(gain, float_size(gain_dtype))) ||
+        !aligned(scales, 4) || !aligned(sums, 4) || (Y && !aligned(Y, float_size(y_dtype))))
+        return PWQ_EINVAL;
+    return hip_status(rms_norm_launch(X, x_dtype, n_tok, d, ldx, residual, ldr, gain, gain_dtype, eps, h_out, ldh, codes,
+                                      ldq, scales, sums, Y, y_dtype, ldy, (hipStream_t)stream));
+}
+
+size_t pwq_quantized_matmul_int8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out) {
+    if (n_tok <= 0 || d_in <= 0 || d_out <= 0 || bad_dim(n_tok) || d_in > TOK_MAX_WIDTH || bad_dim(d_out) ||
+        !w8_size_ok(n_tok, d_in, d_out))
+        return 0;
+    return w8_ws_bytes(n_tok, d_in, d_out);
+}
+
+pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const float* x_scales,
+                                     const int32_t* x_sums, const void* codes, const uint16_t* scales,
+                                     const uint16_t* zeros, int64_t d_out, void* Y, int y_dtype, int64_t ldy, void* ws,
+                                     size_t ws_bytes, void* stream) {
+    if (!float_dtype(y_dtype)) return PWQ_EDTYPE;
+    if (bad_dim(n_tok) || bad_dim(d_out) || d_in < 1 || d_in > TOK_MAX_WIDTH || ldx < d_in || bad_dim(ldx) || ldy < d_out ||
+        bad_dim(ldy))
+        return PWQ_EINVAL;
+    if (n_tok == 0 || d_out == 0) return PWQ_OK;
+    if (!w8_size_ok(n_tok, d_in, d_out)) return PWQ_EINVAL;
+    if (!X || !x_scales || !codes || !scales || !Y || (zeros && !x_sums)) return PWQ_EINVAL;
+    if (!aligned(x_scales, 4) || !aligned(x_sums, 4) || !aligned(scales, 2) || !aligned(zeros, 2) ||
+        !aligned(Y, float_size(y_dtype)))
+        return PWQ_EINVAL;
+    const size_t need = pwq_quantized_matmul_int8_workspace_size(n_tok, d_in, d_out);
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 16))) return PWQ_EWORKSPACE;
+    return hip_status(w8_launch(X, n_tok, d_in, ldx, x_scales, zeros ? x_sums : nullptr, (const uint8_t*)codes, scales,
+                                zeros, d_out, Y, y_dtype, ldy, ws, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -87,6 +87,21 @@ hipError_t w4a16_launch(const uint16_t* X, int64_t T, int64_t n, int64_t ldx, co
                         const uint16_t* scales, const uint16_t* zeros, int64_t m, int group_size, void* Y,
                         int y_dtype, int64_t ldy, void* ws, hipStream_t s);
 
+// 8-bit codes of activations, one scale per token; fused with the RMS norm.
+constexpr int64_t TOK_MAX_WIDTH = 65535;
+hipError_t tok_quant_launch(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx, const float* chan, int8_t* Q,
+                            int64_t ldq, float* S, int32_t* sums, hipStream_t s);
+hipError_t rms_norm_launch(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx, const void* R, int64_t ldr,
+                           const void* G, int g_dtype, double eps, void* H, int64_t ldh, int8_t* Q, int64_t ldq, float* S,
+                           int32_t* sums, void* Y, int y_dtype, int64_t ldy, hipStream_t s);
+
+// Y = (sx X) (sw (C - z))^T on 8-bit codes.
+bool w8_size_ok(int64_t T, int64_t n, int64_t m);
+size_t w8_ws_bytes(int64_t T, int64_t n, int64_t m);
+hipError_t w8_launch(const int8_t* X, int64_t T, int64_t n, int64_t ldx, const float* sx, const int32_t* sums,
+                     const uint8_t* C, const uint16_t* sw, const uint16_t* zeros, int64_t m, void* Y, int y_dtype,
+                     int64_t ldy, void* ws, hipStream_t s);
+
 // Reconstruction MSE.
 size_t mse_ws_bytes(int64_t n_tok, int64_t d_in, int64_t d_out);
 // the split product of the Hessian-route MSE (layers of >= 256 output tiles of 256 x 256):

@@ -76,6 +76,15 @@ _SIGS = {
                                              _c_void_p, _c_void_p, _sz, _c_void_p]),
     "pwq_quantized_matmul_noalloc": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p, _c_void_p,
                                                     _c_void_p, _i64, _i32, _c_void_p, ctypes.c_int, _i64, _c_void_p]),
+    "pwq_quantize_tokens": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p, _c_void_p, _i64, _c_void_p,
+                                           _c_void_p, _c_void_p]),
+    "pwq_rms_norm_quantize": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p,
+                                             ctypes.c_int, ctypes.c_double, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                                             _c_void_p, _c_void_p, ctypes.c_int, _i64, _c_void_p]),
+    "pwq_quantized_matmul_int8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "pwq_quantized_matmul_int8": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                                 _c_void_p, _i64, _c_void_p, ctypes.c_int, _i64, _c_void_p, _sz,
+                                                 _c_void_p]),
     "pwq_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "pwq_profile_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_int64), ctypes.c_int]),
@@ -455,6 +464,131 @@ def quantized_matmul_noalloc(X: torch.Tensor, packed: torch.Tensor, scales: torc
     _check("pwq_quantized_matmul_noalloc", lib().pwq_quantized_matmul_noalloc(
         _p(X), _dtype_code(X), n_tok, d_in, ldx, _p(packed), _p(scales), _p(zeros), d_out, group_size, _p(out),
         _dtype_code(out), ldy, _stream(X)))
+    return out
+
+
+# ------------------------------------------------------------------ 8-bit activations
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _pitch(t: torch.Tensor, name: str, dtypes, dev, shape=None) -> int:
+    """Leading dimension of rows that do not overlap, after checks of type, device and shape."""
+    if t.dtype not in dtypes or t.device != dev or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: expected {' / '.join(str(d) for d in dtypes)} on {dev}"
+                         + (f" of shape {tuple(shape)}" if shape is not None else ""))
+    ld = _rows(t, name)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
+    return ld
+
+
+def _vec(t: torch.Tensor, name: str, dtypes, dev, n: int):
+    """A contiguous vector of n values (n or n x 1) on dev."""
+    if t.dtype not in dtypes or t.device != dev or tuple(t.shape) not in ((n,), (n, 1)) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous {' / '.join(str(d) for d in dtypes)} on {dev}")
+
+
+def _token_outputs(o: dict, T: int, d: int, dev, want_sums: bool):
+    if o.get("codes") is None:
+        o["codes"] = torch.empty((T, d), dtype=torch.int8, device=dev)
+    if o.get("scales") is None:
+        o["scales"] = torch.empty(T, dtype=torch.float32, device=dev)
+    if want_sums and o.get("sums") is None:
+        o["sums"] = torch.empty(T, dtype=torch.int32, device=dev)
+    _vec(o["scales"], "scales", (torch.float32,), dev, T)
+    if want_sums:
+        _vec(o["sums"], "sums", (torch.int32,), dev, T)
+    return _pitch(o["codes"], "codes", (torch.int8,), dev, (T, d))
+
+
+def quantize_tokens(X: torch.Tensor, channel_scale: Optional[torch.Tensor] = None, want_sums: bool = False,
+                    out: Optional[dict] = None) -> dict:
+    """int8 codes of activations with one float32 scale per token: {codes (tokens x d), scales
+    (tokens), sums (int32, with want_sums)}.  ``channel_scale`` (float32, d): X is divided by it
+    column-wise first (awq_search's ``s``).  ``out`` may hold tensors to write into."""
+    dev = X.device
+    ldx = _pitch(X, "X", _FLOATS, dev)
+    T, d = X.shape
+    if channel_scale is not None:
+        _vec(channel_scale, "channel_scale", (torch.float32,), dev, d)
+    o = out if out is not None else {}
+    with torch.cuda.device(dev):
+        ldq = _token_outputs(o, T, d, dev, want_sums)
+        _check("pwq_quantize_tokens", lib().pwq_quantize_tokens(
+            _p(X), _dtype_code(X), T, d, ldx, _p(channel_scale), _p(o["codes"]), ldq, _p(o["scales"]),
+            _p(o["sums"]) if want_sums else None, _stream(X)))
+    return o
+
+
+def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                      eps: float = 1e-5, want_codes: bool = True, want_sums: bool = False, y_dtype=None,
+                      out: Optional[dict] = None) -> dict:
+    """y = h * gain / sqrt(mean(h^2) + eps) with h = X + residual: {codes, scales, sums (with
+    want_sums)} as quantize_tokens gives them for y, h (the sum, in X's type, with a residual;
+    ``out={"h": residual}`` updates it in place), y (with ``y_dtype``: y rounded to that type,
+    e.g. the float16 input of quantized_matmul; ``want_codes=False`` for y alone)."""
+    dev = X.device
+    ldx = _pitch(X, "X", _FLOATS, dev)
+    T, d = X.shape
+    o = out if out is not None else {}
+    ldr = ldh = ldq = ldy = 0
+    if gain is not None:
+        _vec(gain, "gain", _FLOATS, dev, d)
+    with torch.cuda.device(dev):
+        if residual is not None:
+            ldr = _pitch(residual, "residual", (X.dtype,), dev, (T, d))
+            if o.get("h") is None:
+                o["h"] = torch.empty((T, d), dtype=X.dtype, device=dev)
+            ldh = _pitch(o["h"], "h", (X.dtype,), dev, (T, d))
+        if want_codes:
+            ldq = _token_outputs(o, T, d, dev, want_sums)
+        if y_dtype is not None:
+            if o.get("y") is None:
+                o["y"] = torch.empty((T, d), dtype=y_dtype, device=dev)
+            ldy = _pitch(o["y"], "y", (y_dtype,), dev, (T, d))
+        _check("pwq_rms_norm_quantize", lib().pwq_rms_norm_quantize(
+            _p(X), _dtype_code(X), T, d, ldx, _p(residual), ldr, _p(gain), _dtype_code(gain) if gain is not None else 0,
+            float(eps), _p(o["h"]) if residual is not None else None, ldh, _p(o["codes"]) if want_codes else None, ldq,
+            _p(o["scales"]) if want_codes else None, _p(o["sums"]) if want_codes and want_sums else None,
+            _p(o["y"]) if y_dtype is not None else None, _dtype_code(o["y"]) if y_dtype is not None else 0, ldy,
+            _stream(X)))
+    return o
+
+
+def quantized_matmul_int8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                          zeros: Optional[torch.Tensor] = None, x_sums: Optional[torch.Tensor] = None,
+                          out_dtype=torch.float16, out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = (x_scales X) What^T in 8-bit integers: X, x_scales (and x_sums, with zeros) from
+    quantize_tokens or rms_norm_quantize; codes, scales (and zeros) from the RTN or GPTQ calls
+    with group_size 0 (int8 codes, or uint8 codes with zeros)."""
+    dev = X.device
+    ldx = _pitch(X, "X", (torch.int8,), dev)
+    T, d_in = X.shape
+    if codes.dim() != 2 or codes.shape[1] != d_in:
+        raise ValueError(f"codes: expected d_out x {d_in}")
+    d_out = codes.shape[0]
+    if codes.dtype != (torch.int8 if zeros is None else torch.uint8) or codes.device != dev or not codes.is_contiguous():
+        raise ValueError(f"codes: expected contiguous int8 (uint8 with zeros) on {dev}")
+    _vec(x_scales, "x_scales", (torch.float32,), dev, T)
+    _vec(scales, "scales", (torch.float16,), dev, d_out)
+    if zeros is not None:
+        _vec(zeros, "zeros", (torch.int16,), dev, d_out)
+        if x_sums is None:
+            raise ValueError("x_sums: needed with zeros")
+        _vec(x_sums, "x_sums", (torch.int32,), dev, T)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((T, d_out), dtype=out_dtype, device=dev)
+        ldy = _pitch(out, "out", _FLOATS, dev, (T, d_out))
+        nb = lib().pwq_quantized_matmul_int8_workspace_size(T, d_in, d_out)
+        if nb and (ws is None or ws.numel() * ws.element_size() < nb):
+            ws = _ws(nb, dev)
+        if nb and (ws.device != dev or not ws.is_contiguous()):
+            raise ValueError(f"ws: expected contiguous bytes on {dev}")
+        _check("pwq_quantized_matmul_int8", lib().pwq_quantized_matmul_int8(
+            _p(X), T, d_in, ldx, _p(x_scales), _p(x_sums) if zeros is not None else None, _p(codes), _p(scales), _p(zeros),
+            d_out, _p(out), _dtype_code(out), ldy, _p(ws) if nb else None, nb, _stream(X)))
     return out
 
 
