@@ -528,7 +528,7 @@ pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int6
 
 size_t pwq_quantized_matmul_int8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out) {
     if (n_tok <= 0 || d_in <= 0 || d_out <= 0 || bad_dim(n_tok) || d_in > TOK_MAX_WIDTH || bad_dim(d_out) ||
-        !w8_size_ok(n_tok, d_in, d_out))
+        !w8_size_ok(n_tok, d_out))
         return 0;
     return w8_ws_bytes(n_tok, d_in, d_out);
 }
@@ -542,7 +542,7 @@ pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_i
         bad_dim(ldy))
         return PWQ_EINVAL;
     if (n_tok == 0 || d_out == 0) return PWQ_OK;
-    if (!w8_size_ok(n_tok, d_in, d_out)) return PWQ_EINVAL;
+    if (!w8_size_ok(n_tok, d_out)) return PWQ_EINVAL;
     if (!X || !x_scales || !codes || !scales || !Y || (zeros && !x_sums)) return PWQ_EINVAL;
     if (!aligned(x_scales, 4) || !aligned(x_sums, 4) || !aligned(scales, 2) || !aligned(zeros, 2) ||
         !aligned(Y, float_size(y_dtype)))

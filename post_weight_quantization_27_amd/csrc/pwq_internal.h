@@ -96,7 +96,7 @@ hipError_t rms_norm_launch(const void* X, int x_dtype, int64_t T, int64_t d, int
                            int32_t* sums, void* Y, int y_dtype, int64_t ldy, hipStream_t s);
 
 // Y = (sx X) (sw (C - z))^T on 8-bit codes.
-bool w8_size_ok(int64_t T, int64_t n, int64_t m);
+bool w8_size_ok(int64_t T, int64_t m);
 size_t w8_ws_bytes(int64_t T, int64_t n, int64_t m);
 hipError_t w8_launch(const int8_t* X, int64_t T, int64_t n, int64_t ldx, const float* sx, const int32_t* sums,
                      const uint8_t* C, const uint16_t* sw, const uint16_t* zeros, int64_t m, void* Y, int y_dtype,

@@ -39,6 +39,7 @@ struct W8Args {
     int64_t kper;                  // k per split
     int splits, y_dtype;
     int tiles_t, tiles_m;
+    int vec;                       // m and ldy multiples of 4, Y, sw and part aligned for stores of four
 };
 
 __device__ __forceinline__ void w8_store(const W8Args& a, int64_t t, int64_t o, float y) {
@@ -47,14 +48,94 @@ __device__ __forceinline__ void w8_store(const W8Args& a, int64_t t, int64_t o, 
     else ((uint16_t*)a.Y)[i] = a.y_dtype == 1 ? f32_to_f16_bits(y) : f32_to_bf16_bits(y);
 }
 
+// The sum over k of X (C - z) from the sum over the signed bytes
+__device__ __forceinline__ int w8_sum(const W8Args& a, int acc, int64_t t, int64_t o) {
+    if (!a.zeros) return acc;
+    const int z = a.zeros[o];
+    return (int)((uint32_t)acc + (uint32_t)(128 - (z < 255 ? z : 255)) * (uint32_t)a.sums[t]);
+}
+
 // One output: the scale of the row first (the sum times it stays inside float32's range), the
 // token's last.
 __device__ __forceinline__ float w8_value(const W8Args& a, int acc, int64_t t, int64_t o) {
-    if (a.zeros) {
-        const int z = a.zeros[o];
-        acc = (int)((uint32_t)acc + (uint32_t)(128 - (z < 255 ? z : 255)) * (uint32_t)a.sums[t]);
+    return ((float)w8_sum(a, acc, t, o) * f16_bits_to_f32(a.sw[o])) * a.sx[t];
+}
+
+// What four outputs o .. o + 3, and a token, bring to the result.  Kernels load these before
+// their first store: the compiler has to assume that a store may change them.
+struct W8Quad {
+    float w[4];
+    int z[4];                      // 128 - zero
+};
+struct W8Tok {
+    float s;
+    int sum;
+};
+
+__device__ __forceinline__ W8Quad w8_quad(const W8Args& a, int64_t o) {
+    W8Quad q;
+    if (a.vec) {
+        o = o < a.m ? o : a.m - 4;                        // m is a multiple of 4 here
+        const uint2 s = *(const uint2*)(a.sw + o);
+        const uint2 z = a.zeros ? *(const uint2*)(a.zeros + o) : make_uint2(0u, 0u);
+        const uint32_t sb[4] = {s.x & 0xffffu, s.x >> 16, s.y & 0xffffu, s.y >> 16};
+        const uint32_t zb[4] = {z.x & 0xffffu, z.x >> 16, z.y & 0xffffu, z.y >> 16};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q.w[e] = f16_bits_to_f32((uint16_t)sb[e]);
+            q.z[e] = 128 - (int)(zb[e] < 255u ? zb[e] : 255u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t i = o + e < a.m ? o + e : a.m - 1;
+            const int z = a.zeros ? a.zeros[i] : 0;
+            q.w[e] = f16_bits_to_f32(a.sw[i]);
+            q.z[e] = 128 - (z < 255 ? z : 255);
+        }
     }
-    return ((float)acc * f16_bits_to_f32(a.sw[o])) * a.sx[t];
+    return q;
+}
+__device__ __forceinline__ W8Tok w8_tok(const W8Args& a, int64_t t) {
+    t = t < a.T ? t : a.T - 1;
+    return W8Tok{a.sx[t], a.zeros ? a.sums[t] : 0};
+}
+
+// Outputs o .. o + 3 of token t, or their sums over this split of k
+template <bool ZP>
+__device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
+    if (o >= a.m || t >= a.T) return;
+    if (a.splits > 1) {
+        int32_t* p = a.part + ((int64_t)blockIdx.y * a.T + t) * a.m + o;
+        if (a.vec) *(i32x4*)p = acc;
+        else
+            for (int e = 0; e < 4; ++e)
+                if (o + e < a.m) p[e] = acc[e];
+        return;
+    }
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int s = ZP ? (int)((uint32_t)acc[e] + (uint32_t)q.z[e] * (uint32_t)k.sum) : acc[e];
+        y[e] = ((float)s * q.w[e]) * k.s;
+        asm("" : "+v"(y[e]));                             // rounded to float32 before the conversion, in every kernel
+    }
+    const int64_t i = t * a.ldy + o;
+    if (a.vec) {
+        // m and ldy multiples of 4, Y aligned: four outputs in one store
+        if (a.y_dtype == 0) {
+            *(float4*)((float*)a.Y + i) = make_float4(y[0], y[1], y[2], y[3]);
+        } else if (a.y_dtype == 1) {
+            *(uint2*)((uint16_t*)a.Y + i) = make_uint2(f32_to_f16_bits(y[0]) | ((uint32_t)f32_to_f16_bits(y[1]) << 16),
+                                                      f32_to_f16_bits(y[2]) | ((uint32_t)f32_to_f16_bits(y[3]) << 16));
+        } else {
+            *(uint2*)((uint16_t*)a.Y + i) = make_uint2(f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16),
+                                                      f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16));
+        }
+    } else {
+        for (int e = 0; e < 4; ++e)
+            if (o + e < a.m) w8_store(a, t, o + e, y[e]);
+    }
 }
 
 // ------------------------------------------------------------------ any alignment
@@ -165,6 +246,325 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
         }
 }
 
+// ------------------------------------------------------------------ rows of 16-byte multiples
+// BO x BT tile (outputs x tokens), eight waves, v_mfma_i32_16x16x64_i8 with the codes as the row
+// operand, so that a lane ends with four consecutive outputs of one token.
+//
+// Operand rows go straight from memory into LDS (global_load_lds, 16 bytes a lane) in stages of
+// BK k.  Row r of a stage keeps its 16-byte chunk c at a position xor-ed with a function of r
+// chosen so that the 16 lanes which a 16-byte LDS read serves at a time (lanes 0-3, 12-15,
+// 20-23, 24-27 of each half wave, and the rest) hit 16 different bank groups: the counters show
+// no conflict.
+//
+// The waves work in two groups of four, one half step apart: while one group reads its fragments
+// of a stage (and starts the copies of a later one), the other runs its MFMAs, with a barrier
+// between the half steps.  Each SIMD holds one wave of each group, so its matrix unit always
+// has the work of one of them.
+//   KG = 1: both groups take every stage, each its half of the tile (WO x 8 / WO waves): the
+//           least LDS traffic of the copies, for large tiles.
+//   KG = 2: each group takes every other stage of k for the whole tile (WO x 4 / WO waves), with
+//           stages of its own that its own waves copy; the two sums meet in LDS at the end.
+//           The wave tiles are twice as large, which saves a third of the LDS reads on tiles
+//           that eight waves would cut too small.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+__device__ const uint4 w8_zeros = {0u, 0u, 0u, 0u};
+
+// s_waitcnt with only the vector-memory count constrained: vmcnt <= N
+template <int N>
+__device__ __forceinline__ void w8_wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+// all LDS reads of this wave have arrived
+__device__ __forceinline__ void w8_wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+// workgroup barrier without a fence: copies stay in flight across it
+__device__ __forceinline__ void w8_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// position of chunk c in row r of a stage
+template <int BK>
+__device__ __forceinline__ int w8_pos(int r, int c) {
+    return BK == 64 ? c ^ ((4 - (r >> 2)) & 3) : (BK == 128 ? c ^ ((r >> 1) & 7) : c ^ (r & 15));
+}
+
+// bid -> tile: consecutive workgroups go to different XCDs, so each XCD takes a contiguous share
+// of the tiles, in groups of up to 8 output tiles by all token tiles
+__device__ __forceinline__ void w8_map(const W8Args& a, int bid, int& to, int& tt) {
+    const int nt = a.tiles_t * a.tiles_m;
+    const int x = bid & 7, per = nt >> 3, rem = nt & 7;
+    const int id = x * per + (x < rem ? x : rem) + (bid >> 3);
+    const int g = id / (8 * a.tiles_t);
+    const int rows = a.tiles_m - 8 * g < 8 ? a.tiles_m - 8 * g : 8;
+    const int in = id - g * 8 * a.tiles_t;
+    tt = in / rows;
+    to = 8 * g + in - tt * rows;
+}
+
+template <int BO, int BT, int BK, int NST, int WO, int KG, bool ZP>
+__global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
+    constexpr int NW = 8 / KG, WT = NW / WO;              // waves that share a stage
+    constexpr int FO = BO / WO / 16, FT = BT / WT / 16, KS = BK / 64;
+    constexpr int ROWB = 1024 / BK;                       // rows per copy instruction of a wave
+    constexpr int L = (BO + BT) / ROWB / NW;              // copies per wave and stage
+    constexpr int ST = (BO + BT) * BK;
+    static_assert(L * NW * ROWB == BO + BT && L * (NST - 2) < 64 && KG * NST * ST <= 163840, "tile");
+    static_assert(KG == 1 || (FO % 2 == 0 && 8 * FO / 2 * FT * 1024 <= 2 * NST * ST), "the groups' sums fit the stages");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[KG * NST * ST];
+    int to, tt;
+    w8_map(a, blockIdx.x, to, tt);
+    const int64_t o0 = (int64_t)to * BO, t0 = (int64_t)tt * BT;
+    const int lane = threadIdx.x & 63, wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = KG == 2 ? wave8 & 3 : wave8, grp = wave8 >> 2;
+    const int wo = wave / WT, wt = wave % WT;
+    uint8_t* const lds = smem + (KG == 2 ? grp * (NST * ST) : 0);
+    // this wave's k: from kbeg in steps of KG BK; nk of its stages, the first nfull of which end
+    // inside the rows; nmax steps for everybody
+    const int64_t kend = (blockIdx.y + 1) * a.kper < a.n ? (blockIdx.y + 1) * a.kper : a.n;
+    const int64_t kbeg = (int64_t)blockIdx.y * a.kper + (KG == 2 ? grp * BK : 0);
+    const int64_t klen = kend - kbeg;
+    const int nk = klen > 0 ? (int)((klen + KG * BK - 1) / (KG * BK)) : 0;
+    const int nfull = klen >= BK ? (int)((klen - BK) / (KG * BK)) + 1 : 0;
+    const int nmax = KG == 2 ? (int)((kend - (int64_t)blockIdx.y * a.kper + KG * BK - 1) / (KG * BK)) : nk;
+
+    // copy j of this wave: ROWB rows from row q ROWB on, q = wave L + j, of the codes' BO rows
+    // followed by the activations' BT; a lane brings the chunk that its position holds.  Rows
+    // past the matrices repeat the last one (their outputs are not stored).
+    const uint8_t* src[L];
+    bool is_x[L];
+    int chunk[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const int r = (wave * L + j) * ROWB + lane / (BK / 16);
+        chunk[j] = w8_pos<BK>(r & 15, lane % (BK / 16));  // the xor undoes itself
+        is_x[j] = (wave * L + j) * ROWB >= BO;
+        if (is_x[j]) {
+            const int64_t t = t0 + r - BO;
+            src[j] = (const uint8_t*)a.X + (t < a.T ? t : a.T - 1) * a.ldx + kbeg + 16 * chunk[j];
+        } else {
+            const int64_t o = o0 + r;
+            src[j] = a.C + (o < a.m ? o : a.m - 1) * a.n + kbeg + 16 * chunk[j];
+        }
+    }
+    // The order of k is free, so tiles that live on the codes' traffic start at different k:
+    // where d_in is a multiple of 4096, rows that are read at the same k in step all come
+    // from the same few memory channels (one token by 8192 x 28672 outputs: 52 us without, 44
+    // with; at 8320 inputs 43 either way).  Large token tiles share X by k instead and start
+    // together.
+    constexpr int ROT = BT <= 128 ? 3 : 0;
+    const int rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
+    auto copy = [&](int it) {
+        uint8_t* S = lds + (it % NST) * ST + wave * (L * 1024);
+        const int pos = it + rot;
+        const int64_t k = (int64_t)(ROT && pos >= nfull ? pos - nfull : pos) * (KG * BK);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            __builtin_amdgcn_global_load_lds((const void*)(src[j] + k), (lds_ptr_t)(S + j * 1024), 16, 0, 0);
+    };
+    // the last stage where it ends past the rows: zeros for the activations, any bytes for the codes
+    auto copy_end = [&](int it) {
+        uint8_t* S = lds + (it % NST) * ST + wave * (L * 1024);
+        const int64_t k = (int64_t)it * (KG * BK);
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const bool in = kbeg + k + 16 * chunk[j] < kend;
+            const uint8_t* p = in ? src[j] + k : (is_x[j] ? (const uint8_t*)&w8_zeros : src[j] - 16 * chunk[j]);
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_ptr_t)(S + j * 1024), 16, 0, 0);
+        }
+    };
+
+    i32x4 acc[FO][FT];
+#pragma unroll
+    for (int i = 0; i < FO; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < NST - 1; ++q) {
+        if (q < nfull) copy(q);
+        else if (q < nk) copy_end(q);
+    }
+    if (nk >= NST - 1) w8_wait_vm<L * (NST - 2)>();
+    else w8_wait_vm<0>();
+    w8_barrier();
+    if (grp == 1) w8_barrier();                           // the second group runs half a step behind
+
+    const int r = lane & 15, c = lane >> 4;
+    const uint8_t* la[KS];
+    const uint8_t* lb[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const int o = r * BK + 16 * w8_pos<BK>(r, 4 * ks + c);
+        la[ks] = lds + wo * (BO / WO) * BK + o;
+        lb[ks] = lds + (BO + wt * (BT / WT)) * BK + o;
+    }
+    auto step = [&](int it, auto start_copy) {
+        const int st = (it % NST) * ST;
+        i32x4 fo[KS][FO], ft[KS][FT];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int j = 0; j < FT; ++j) ft[ks][j] = *(const i32x4*)(lb[ks] + st + j * 16 * BK);
+#pragma unroll
+            for (int i = 0; i < FO; ++i) fo[ks][i] = *(const i32x4*)(la[ks] + st + i * 16 * BK);
+        }
+        // stage it + NST - 1 takes the place of stage it - 1: the group ahead finished reading it
+        // a step ago, the group behind before the barrier just passed.  This wave's copies of
+        // stage it + 1 have landed before the barrier that lets the group ahead read it.
+        start_copy();
+        w8_wait_lds();
+        if constexpr (ZP) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int i = 0; i < FO; ++i) {
+                    // waited for above: the value passes through an empty asm so that no use of it moves up
+                    asm volatile("" : "+v"(fo[ks][i]));
+                    fo[ks][i] ^= (int)0x80808080;
+                }
+        }
+        w8_barrier();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int i = 0; i < FO; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fo[ks][i], ft[ks][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        w8_barrier();
+    };
+    int it = 0;
+    for (; it + NST - 1 < nfull; ++it)
+        step(it, [&] {
+            copy(it + NST - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            w8_wait_vm<L * (NST - 2)>();
+        });
+    for (; it < nk; ++it)
+        step(it, [&] {
+            if (it + NST - 1 < nk) copy_end(it + NST - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            w8_wait_vm<0>();
+        });
+    if (KG == 2 && nk < nmax) {                           // the other group's last stage
+        w8_barrier();
+        w8_barrier();
+    }
+    if (grp == 0) w8_barrier();
+
+    // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
+    // second; each takes the other's sums of its half from LDS
+    constexpr int FH = KG == 2 ? FO / 2 : FO;
+    if constexpr (KG == 2) {
+        i32x4* x = (i32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
+        w8_barrier();                                     // every wave has read its last stage
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) {
+                const i32x4 lo = acc[i][j], hi = acc[FH + i][j];
+                i32x4 send, keep;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    send[e] = grp == 0 ? hi[e] : lo[e];
+                    keep[e] = grp == 0 ? lo[e] : hi[e];
+                }
+                x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
+                acc[i][j] = keep;
+            }
+        w8_wait_lds();
+        w8_barrier();
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
+    }
+    W8Quad q[FH];
+    W8Tok tok[FT];
+    const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0) + 4 * c, tb = t0 + wt * (BT / WT) + r;
+#pragma unroll
+    for (int i = 0; i < FH; ++i) q[i] = w8_quad(a, ob + 16 * i);
+#pragma unroll
+    for (int j = 0; j < FT; ++j) tok[j] = w8_tok(a, tb + 16 * j);
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+#pragma unroll
+        for (int i = 0; i < FH; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
+}
+
+// ------------------------------------------------------------------ few tokens
+// Few tokens by short rows, where a launch's latency counts, and one token, where the codes are the
+// traffic: a workgroup owns 16 output rows by 16 tokens, its eight waves share k in turns of
+// 64 U, every lane loads its fragments (16 bytes of one row) straight into registers, those of a
+// turn while the turn before is multiplied, and the waves' sums meet in LDS.  No staging: a code
+// is used once, and X comes from L2.  Loads past the rows or tokens take a 16-byte block of
+// zeros as their address, so none waits behind a branch.
+template <int U, bool ZP>
+__global__ __launch_bounds__(512) void w8_row_kernel(W8Args a) {
+    __shared__ i32x4 red[8][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, c = lane >> 4;
+    const int64_t o0 = (int64_t)blockIdx.x * 16, t = (int64_t)blockIdx.z * 16 + r;
+    const uint8_t* crow = a.C + (o0 + r < a.m ? o0 + r : a.m - 1) * a.n;
+    const bool xin = t < a.T;
+    const uint8_t* xrow = (const uint8_t*)a.X + (xin ? t : 0) * a.ldx;
+    const W8Quad q = w8_quad(a, o0 + 4 * c);              // ahead of the loop, for the end
+    const W8Tok tok = w8_tok(a, t);
+    i32x4 acc = {0, 0, 0, 0};
+    i32x4 fo[2][U], ft[2][U];
+    const int n = (int)a.n;
+    auto load = [&](i32x4 (&co)[U], i32x4 (&ct)[U], int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = k0 + 64 * u + 16 * c;
+            const bool in = k < n;
+            co[u] = __builtin_nontemporal_load((const i32x4*)(crow + (in ? k : 0)));
+            ct[u] = *(const i32x4*)(in && xin ? xrow + k : (const uint8_t*)&w8_zeros);
+        }
+    };
+    auto mult = [&](i32x4 (&co)[U], i32x4 (&ct)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (ZP) co[u] ^= (int)0x80808080;
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(co[u], ct[u], acc, 0, 0, 0);
+        }
+    };
+    // turns of the whole workgroup, from a different one on each (see the tiles' order of k)
+    constexpr int TURN = 8 * 64 * U;
+    const int turns = (n + TURN - 1) / TURN;
+    int at = (int)(blockIdx.x % (unsigned)turns) * TURN + wave * (64 * U);
+    auto next = [&] {
+        const int k0 = at;
+        at = at + TURN < turns * TURN ? at + TURN : wave * (64 * U);
+        return k0;
+    };
+    load(fo[0], ft[0], next());
+    int left = turns;
+    for (; left > 2; left -= 2) {
+        load(fo[1], ft[1], next());
+        mult(fo[0], ft[0]);
+        load(fo[0], ft[0], next());
+        mult(fo[1], ft[1]);
+    }
+    if (left == 2) {
+        load(fo[1], ft[1], next());
+        mult(fo[0], ft[0]);
+        mult(fo[1], ft[1]);
+    } else {
+        mult(fo[0], ft[0]);
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) acc += red[w][lane];
+    w8_out4<ZP>(a, acc, t, o0 + 4 * c, q, tok);
+}
+
 // the splits' sums of each output, scaled
 __global__ __launch_bounds__(256) void w8_join_kernel(W8Args a) {
     const int64_t size = a.T * a.m;
@@ -176,49 +576,153 @@ __global__ __launch_bounds__(256) void w8_join_kernel(W8Args a) {
     }
 }
 
+// ------------------------------------------------------------------ which kernel
 struct W8Plan {
+    int kind;                      // W8_ANY, W8_ROW2, W8_ROW4 or an index into w8_tiles
     int splits;
     int64_t kper;
 };
+constexpr int W8_ANY = -1, W8_ROW2 = -2, W8_ROW4 = -3;
 
-// Splits of k until about two workgroups per compute unit run, each with at least W8_SPLIT_MIN_K
-W8Plan w8_plan(int64_t T, int64_t n, int64_t m) {
+// k over `s` splits in whole steps of `step`
+W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
+    const int64_t kper = cdiv(cdiv(n, s < 1 ? 1 : s), step) * step;
+    return W8Plan{kind, (int)cdiv(n, kper), kper};
+}
+
+// Any alignment: splits of k until about two workgroups per compute unit run, each with at least
+// W8_SPLIT_MIN_K.
+W8Plan w8_plan_any(int64_t T, int64_t n, int64_t m) {
     const int64_t tiles = cdiv(T, G_TILE) * cdiv(m, G_TILE);
     int64_t s = cdiv(512, tiles);
     if (s > n / W8_SPLIT_MIN_K) s = n / W8_SPLIT_MIN_K;
-    if (s < 1) s = 1;
-    const int64_t kper = cdiv(cdiv(n, s), G_BK) * G_BK;
-    return W8Plan{(int)cdiv(n, kper), kper};
+    return w8_split(W8_ANY, n, s, G_BK);
+}
+
+// The tiles, and what one costs on this chip: every compute unit holds one workgroup, which takes
+// `fixed` microseconds and `step` more for each 128 k (measured with all 256 at work on 8192 k of
+// weights that come from memory; fewer workgroups save a fifth of a step at most, so rounds of
+// 256 are what counts).
+struct W8TileCost {
+    int bo, bt, bk;
+    float fixed, step;
+};
+constexpr W8TileCost w8_tiles[] = {
+    {256, 256, 64, 8.f, 1.60f},    // 2.5 POP/s on 8192^3
+    {128, 256, 128, 5.f, 0.85f},
+    {128, 128, 128, 3.f, 0.60f},
+    {128, 64, 128, 2.5f, 0.46f},
+    {64, 64, 128, 2.f, 0.31f},
+};
+constexpr int W8_TILES = sizeof(w8_tiles) / sizeof(w8_tiles[0]);
+
+// The least estimate of: rounds of tiles, over 1 to 8 splits of k whose sums a second launch
+// joins; no less than memory takes for the operands (5.4 TB/s); or one row kernel, whose time is
+// the codes' traffic (5.4 TB/s, once per 16 tokens, and up to 0.45 of it again for X) and the
+// latency of its turns.  Measured over 88 shapes (768 .. 28672 inputs and outputs, 1 .. 2048
+// tokens), the choice is the fastest of the kernels or within 12 % of it; with 128 x 128 tiles
+// alone the same shapes take up to 4 times as long (16 tokens by 28672 inputs: 102 against
+// 45 us; 1 token by 768 x 768: 8 against 3 us).
+W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
+    const double bytes = ((double)T * n + (double)m * n + 2.0 * T * m) * 1e-6;          // MB
+    const double mem = bytes / 5.4 + 2.0;
+    W8Plan best{W8_ANY, 1, n};
+    double least = 1e30;
+    for (int i = 0; i < W8_TILES; ++i) {
+        const W8TileCost& c = w8_tiles[i];
+        const int64_t tiles = cdiv(T, c.bt) * cdiv(m, c.bo);
+        for (int64_t s = 1; s <= 8; s *= 2) {
+            if (s > 1 && n / s < W8_SPLIT_MIN_K) break;
+            const W8Plan p = w8_split(i, n, s, c.bk);
+            if (s > 1 && p.splits < s) continue;
+            const double rounds = (double)cdiv(tiles * p.splits, 256);
+            const double work = 2.0 + rounds * (c.fixed + c.step * (double)p.kper / 128.0);
+            double t = (work > mem ? work : mem) + 0.05 * work;
+            if (p.splits > 1) t += 4.0 + 2.0 * (double)p.splits * T * m * 4e-6 / 4.0;
+            if (t < least) { least = t; best = p; }
+        }
+    }
+    if (T <= 1024) {
+        const double traffic = (double)m * n * 1e-6 * (double)cdiv(T, 16) * (1.0 + 0.45 * (T < 16 ? T : 16) / 16.0) / 5.4;
+        const double t = 2.2 + traffic + 0.2 * (double)cdiv(n, 1024);
+        // turns of 8 waves x 128 k fill the waves of short rows, turns of 256 k keep more loads
+        // in flight on long ones (28672 x 1024: 8.6 against 12 us; 8192 x 8192: 16.1 against 15.8)
+        if (t < least) best = w8_split(n < 4096 ? W8_ROW2 : W8_ROW4, n, 1, 64);
+    }
+    return best;
+}
+
+template <int BO, int BT, int BK, int NST, int WO, int KG>
+hipError_t w8_tile_go(W8Args a, hipStream_t s) {
+    a.tiles_m = (int)cdiv(a.m, BO);
+    a.tiles_t = (int)cdiv(a.T, BT);
+    const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
+    if (a.zeros) hipLaunchKernelGGL((w8_tile_kernel<BO, BT, BK, NST, WO, KG, true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((w8_tile_kernel<BO, BT, BK, NST, WO, KG, false>), grid, dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int U>
+hipError_t w8_row_go(const W8Args& a, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(a.m, 16), 1, (unsigned)cdiv(a.T, 16));
+    if (a.zeros) hipLaunchKernelGGL((w8_row_kernel<U, true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((w8_row_kernel<U, false>), grid, dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t w8_any_go(W8Args a, hipStream_t s) {
+    a.tiles_m = (int)cdiv(a.m, G_TILE);
+    a.tiles_t = (int)cdiv(a.T, G_TILE);
+    const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
+    if (a.zeros) hipLaunchKernelGGL(w8_any_kernel<true>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(w8_any_kernel<false>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t w8_run(W8Args a, const W8Plan& p, hipStream_t s) {
+    a.splits = p.splits;
+    a.kper = p.kper;
+    hipError_t e;
+    switch (p.kind) {
+        case 0: e = w8_tile_go<256, 256, 64, 5, 4, 1>(a, s); break;
+        case 1: e = w8_tile_go<128, 256, 128, 3, 2, 1>(a, s); break;
+        case 2: e = w8_tile_go<128, 128, 128, 4, 2, 1>(a, s); break;
+        case 3: e = w8_tile_go<128, 64, 128, 3, 2, 2>(a, s); break;
+        case 4: e = w8_tile_go<64, 64, 128, 4, 2, 2>(a, s); break;
+        case W8_ROW2: e = w8_row_go<2>(a, s); break;
+        case W8_ROW4: e = w8_row_go<4>(a, s); break;
+        default: e = w8_any_go(a, s); break;
+    }
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t blocks = cdiv(a.T * a.m, 256);
+    hipLaunchKernelGGL(w8_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-bool w8_size_ok(int64_t T, int64_t n, int64_t m) {
-    // work-items of a launch are counted in 32 bits
-    return cdiv(T, G_TILE) * cdiv(m, G_TILE) < ((int64_t)1 << 24);
+bool w8_size_ok(int64_t T, int64_t m) {
+    // work-items of a launch are counted in 32 bits: workgroups of 512 for tiles of 64 x 64 at least
+    return cdiv(T, 64) * cdiv(m, 64) < ((int64_t)1 << 23) && cdiv(m, 16) < ((int64_t)1 << 23);
 }
 
 size_t w8_ws_bytes(int64_t T, int64_t n, int64_t m) {
-    const W8Plan p = w8_plan(T, n, m);
-    return p.splits > 1 ? (size_t)p.splits * (size_t)T * (size_t)m * sizeof(int32_t) : 0;
+    // rows of 16-byte multiples or not is the pointers' affair, so there is room for either plan
+    const W8Plan any = w8_plan_any(T, n, m);
+    const W8Plan fast = n % 16 == 0 ? w8_plan_fast(T, n, m) : any;
+    const int splits = any.splits > fast.splits ? any.splits : fast.splits;
+    return splits > 1 ? (size_t)splits * (size_t)T * (size_t)m * sizeof(int32_t) : 0;
 }
 
 hipError_t w8_launch(const int8_t* X, int64_t T, int64_t n, int64_t ldx, const float* sx, const int32_t* sums,
                      const uint8_t* C, const uint16_t* sw, const uint16_t* zeros, int64_t m, void* Y, int y_dtype,
                      int64_t ldy, void* ws, hipStream_t s) {
-    const W8Plan p = w8_plan(T, n, m);
     W8Args a{};
     a.X = X; a.sx = sx; a.sums = sums; a.C = C; a.sw = sw; a.zeros = zeros; a.Y = Y; a.part = (int32_t*)ws;
-    a.ldx = ldx; a.ldy = ldy; a.T = T; a.n = n; a.m = m; a.kper = p.kper; a.splits = p.splits; a.y_dtype = y_dtype;
-    a.tiles_t = (int)cdiv(T, G_TILE); a.tiles_m = (int)cdiv(m, G_TILE);
-    const dim3 grid((unsigned)(a.tiles_t * (int64_t)a.tiles_m), (unsigned)p.splits);
-    if (zeros) hipLaunchKernelGGL(w8_any_kernel<true>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(w8_any_kernel<false>, grid, dim3(256), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t blocks = cdiv(T * m, 256);
-    hipLaunchKernelGGL(w8_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    a.ldx = ldx; a.ldy = ldy; a.T = T; a.n = n; a.m = m; a.y_dtype = y_dtype;
+    a.vec = m % 4 == 0 && ldy % 4 == 0 && aligned(Y, y_dtype == 0 ? 16 : 8) && aligned(sw, 8) && aligned(zeros, 8);
+    const bool rows16 = n % 16 == 0 && ldx % 16 == 0 && aligned(X, 16) && aligned(C, 16);
+    return w8_run(a, rows16 ? w8_plan_fast(T, n, m) : w8_plan_any(T, n, m), s);
 }
 
 }  // namespace pwq

@@ -305,6 +305,51 @@ def test_quantized_matmul_int8_largest_sums(pwq, T, n):
         assert torch.all(Y == float(np.float32(-128.0 * n * (c - z)))).item()
 
 
+@pytest.mark.parametrize("T,n,m,zp,odt", [(2000, 2064, 8100, False, "bf16"), (4096, 528, 4100, True, "f16"),
+                                          (1000, 8208, 2100, True, "f32"), (70, 28672, 2000, True, "f32"),
+                                          (300, 28672, 2000, False, "f16"), (1000, 65520, 300, True, "f32"),
+                                          (40, 2064, 8100, False, "f32"), (2, 65520, 1000, True, "bf16"),
+                                          (3, 28672, 4096, False, "f32"), (129, 8208, 384, True, "f32"),
+                                          (515, 1024, 28672, False, "bf16"), (200, 5000, 3000, True, "f32")])
+def test_quantized_matmul_int8_large_sampled(pwq, T, n, m, zp, odt):
+    """Sizes that take the larger tiles and splits of k, ragged in every dimension: the oracle on
+    sampled tokens by sampled outputs, the edges among them."""
+    rng = np.random.default_rng(T + n + m)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(n)
+    X = torch.randint(-128, 128, (T, n), generator=g, device=DEV, dtype=torch.int8)
+    C = torch.randint(-128, 128, (m, n), generator=g, device=DEV, dtype=torch.int8)
+    z = None
+    if zp:
+        C = C.view(torch.uint8)
+        z = torch.randint(0, 256, (m, 1), generator=g, device=DEV, dtype=torch.int16)
+    sx = torch.rand(T, generator=g, device=DEV) * 0.01 + 0.001
+    sw = (torch.rand(m, 1, generator=g, device=DEV) * 0.003 + 0.0005).half()
+    Y = pwq.quantized_matmul_int8(X, sx, C, sw, zeros=z, x_sums=X.sum(1, dtype=torch.int32) if zp else None,
+                                  out_dtype=TYPES[odt])
+    ts = np.unique(np.concatenate([rng.integers(0, T, 40), [0, T - 1]]))
+    os_ = np.unique(np.concatenate([rng.integers(0, m, 90), [0, 1, m - 2, m - 1]]))
+    ti, oi = torch.from_numpy(ts).to(DEV), torch.from_numpy(os_).to(DEV)
+    want = O.quantized_matmul_int8(X[ti].cpu().numpy(), sx[ti].cpu().numpy(), C[oi].cpu().numpy(), sw[oi].cpu().numpy(),
+                                   zeros=None if z is None else z[oi].cpu().numpy())
+    err = np.abs(f64(Y[ti][:, oi]) - want)
+    tol = np.abs(want) * 3.001 * 2.0 ** -24 + half_step(want, TYPES[odt])
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3f} of the bound"
+    # every other output against the same call on other rows: another kernel, the same bits
+    half = pwq.quantized_matmul_int8(X[:T // 2], sx[:T // 2], C, sw, zeros=z,
+                                     x_sums=X[:T // 2].sum(1, dtype=torch.int32) if zp else None, out_dtype=TYPES[odt])
+    assert torch.equal(Y[:T // 2], half)
+    one = pwq.quantized_matmul_int8(X[-1:], sx[-1:], C, sw, zeros=z, x_sums=X[-1:].sum(1, dtype=torch.int32) if zp else None,
+                                    out_dtype=TYPES[odt])
+    assert torch.equal(Y[-1:], one)
+    odd = torch.zeros(C.numel() + 1, dtype=C.dtype, device=DEV)[1:].view(m, n)
+    odd.copy_(C)
+    few = min(T, 130)
+    got = pwq.quantized_matmul_int8(X[:few], sx[:few], odd, sw, zeros=z,
+                                    x_sums=X[:few].sum(1, dtype=torch.int32) if zp else None, out_dtype=TYPES[odt])
+    assert torch.equal(Y[:few], got)
+
+
 def test_quantized_matmul_int8_scales(pwq):
     """Scales at the ends of their ranges: a token of scale 0 or NaN, products that a scale alone
     would carry out of float32's range."""
