@@ -468,37 +468,70 @@ def quantized_matmul_noalloc(X: torch.Tensor, packed: torch.Tensor, scales: torc
 
 
 # ------------------------------------------------------------------ 8-bit activations
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+# One token's calls cost less on the GPU than here, so these marshal with few torch calls: plain
+# integers for pointers, the raw stream, a device switch only where another is current, and
+# checks of given tensors alone.
+_CODES = {torch.float32: PWQ_F32, torch.float16: PWQ_F16, torch.bfloat16: PWQ_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _bad(name: str, want: str):
+    raise ValueError(f"{name}: expected {want}")
 
 
 def _pitch(t: torch.Tensor, name: str, dtypes, dev, shape=None) -> int:
-    """Leading dimension of rows that do not overlap, after checks of type, device and shape."""
-    if t.dtype not in dtypes or t.device != dev or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: expected {' / '.join(str(d) for d in dtypes)} on {dev}"
-                         + (f" of shape {tuple(shape)}" if shape is not None else ""))
-    ld = _rows(t, name)
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)})")
-    return ld
+    """Leading dimension of a matrix of `dtypes` on dev (of `shape`) whose rows do not overlap."""
+    sh = t.shape
+    if t.dtype not in dtypes or t.device != dev or len(sh) != 2 or (shape is not None and sh != shape):
+        _bad(name, f"a {'matrix' if shape is None else tuple(shape)} of {' / '.join(map(str, dtypes))} on {dev}")
+    s0, s1 = t.stride()
+    if s1 != 1 and sh[1] > 1:
+        _bad(name, "contiguous columns")
+    if s0 < sh[1]:
+        if sh[0] > 1:
+            _bad(name, f"rows that do not overlap (stride {s0})")
+        return sh[1]
+    return s0
 
 
-def _vec(t: torch.Tensor, name: str, dtypes, dev, n: int):
-    """A contiguous vector of n values (n or n x 1) on dev."""
-    if t.dtype not in dtypes or t.device != dev or tuple(t.shape) not in ((n,), (n, 1)) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous {' / '.join(str(d) for d in dtypes)} on {dev}")
+def _vec(t: torch.Tensor, name: str, dtypes, dev, n: int) -> int:
+    """Address of a contiguous vector of n values (n or n x 1) on dev."""
+    if t.dtype not in dtypes or t.device != dev or t.shape not in ((n,), (n, 1)) or not t.is_contiguous():
+        _bad(name, f"{n} contiguous {' / '.join(map(str, dtypes))} on {dev}")
+    return t.data_ptr()
+
+
+def _on(X: torch.Tensor, call, *args):
+    """call(*args) with X's device current and its current stream as the last argument."""
+    dev = X.device
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    if torch.cuda.current_device() == dev.index:
+        return call(*args, _raw_stream(dev.index))
+    with torch.cuda.device(dev):
+        return call(*args, _raw_stream(dev.index))
 
 
 def _token_outputs(o: dict, T: int, d: int, dev, want_sums: bool):
-    if o.get("codes") is None:
-        o["codes"] = torch.empty((T, d), dtype=torch.int8, device=dev)
-    if o.get("scales") is None:
-        o["scales"] = torch.empty(T, dtype=torch.float32, device=dev)
-    if want_sums and o.get("sums") is None:
-        o["sums"] = torch.empty(T, dtype=torch.int32, device=dev)
-    _vec(o["scales"], "scales", (torch.float32,), dev, T)
+    """(codes, its pitch, scales, sums): addresses in o's tensors, which are made where missing."""
+    q, ldq = o.get("codes"), d
+    if q is None:
+        q = o["codes"] = torch.empty((T, d), dtype=torch.int8, device=dev)
+    else:
+        ldq = _pitch(q, "codes", (torch.int8,), dev, (T, d))
+    s = o.get("scales")
+    if s is None:
+        s = o["scales"] = torch.empty((T,), dtype=torch.float32, device=dev)
+    else:
+        _vec(s, "scales", (torch.float32,), dev, T)
+    n = None
     if want_sums:
-        _vec(o["sums"], "sums", (torch.int32,), dev, T)
-    return _pitch(o["codes"], "codes", (torch.int8,), dev, (T, d))
+        n = o.get("sums")
+        if n is None:
+            n = o["sums"] = torch.empty((T,), dtype=torch.int32, device=dev)
+        n = _vec(n, "sums", (torch.int32,), dev, T)
+    return q.data_ptr(), ldq, s.data_ptr(), n
 
 
 def quantize_tokens(X: torch.Tensor, channel_scale: Optional[torch.Tensor] = None, want_sums: bool = False,
@@ -507,16 +540,14 @@ def quantize_tokens(X: torch.Tensor, channel_scale: Optional[torch.Tensor] = Non
     (tokens), sums (int32, with want_sums)}.  ``channel_scale`` (float32, d): X is divided by it
     column-wise first (awq_search's ``s``).  ``out`` may hold tensors to write into."""
     dev = X.device
-    ldx = _pitch(X, "X", _FLOATS, dev)
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    ldx = _pitch(X, "X", _CODES, dev)
     T, d = X.shape
-    if channel_scale is not None:
-        _vec(channel_scale, "channel_scale", (torch.float32,), dev, d)
+    c = None if channel_scale is None else _vec(channel_scale, "channel_scale", (torch.float32,), dev, d)
     o = out if out is not None else {}
-    with torch.cuda.device(dev):
-        ldq = _token_outputs(o, T, d, dev, want_sums)
-        _check("pwq_quantize_tokens", lib().pwq_quantize_tokens(
-            _p(X), _dtype_code(X), T, d, ldx, _p(channel_scale), _p(o["codes"]), ldq, _p(o["scales"]),
-            _p(o["sums"]) if want_sums else None, _stream(X)))
+    q, ldq, s, n = _token_outputs(o, T, d, dev, want_sums)
+    _check("pwq_quantize_tokens", _on(X, lib().pwq_quantize_tokens, X.data_ptr(), _CODES[X.dtype], T, d, ldx, c, q, ldq, s, n))
     return o
 
 
@@ -528,30 +559,35 @@ def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, resi
     ``out={"h": residual}`` updates it in place), y (with ``y_dtype``: y rounded to that type,
     e.g. the float16 input of quantized_matmul; ``want_codes=False`` for y alone)."""
     dev = X.device
-    ldx = _pitch(X, "X", _FLOATS, dev)
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    ldx = _pitch(X, "X", _CODES, dev)
     T, d = X.shape
     o = out if out is not None else {}
+    g = None if gain is None else _vec(gain, "gain", _CODES, dev, d)
+    r = h = q = s = n = y = None
     ldr = ldh = ldq = ldy = 0
-    if gain is not None:
-        _vec(gain, "gain", _FLOATS, dev, d)
-    with torch.cuda.device(dev):
-        if residual is not None:
-            ldr = _pitch(residual, "residual", (X.dtype,), dev, (T, d))
-            if o.get("h") is None:
-                o["h"] = torch.empty((T, d), dtype=X.dtype, device=dev)
-            ldh = _pitch(o["h"], "h", (X.dtype,), dev, (T, d))
-        if want_codes:
-            ldq = _token_outputs(o, T, d, dev, want_sums)
-        if y_dtype is not None:
-            if o.get("y") is None:
-                o["y"] = torch.empty((T, d), dtype=y_dtype, device=dev)
-            ldy = _pitch(o["y"], "y", (y_dtype,), dev, (T, d))
-        _check("pwq_rms_norm_quantize", lib().pwq_rms_norm_quantize(
-            _p(X), _dtype_code(X), T, d, ldx, _p(residual), ldr, _p(gain), _dtype_code(gain) if gain is not None else 0,
-            float(eps), _p(o["h"]) if residual is not None else None, ldh, _p(o["codes"]) if want_codes else None, ldq,
-            _p(o["scales"]) if want_codes else None, _p(o["sums"]) if want_codes and want_sums else None,
-            _p(o["y"]) if y_dtype is not None else None, _dtype_code(o["y"]) if y_dtype is not None else 0, ldy,
-            _stream(X)))
+    if residual is not None:
+        ldr = _pitch(residual, "residual", (X.dtype,), dev, (T, d))
+        r, t, ldh = residual.data_ptr(), o.get("h"), d
+        if t is None:
+            t = o["h"] = torch.empty((T, d), dtype=X.dtype, device=dev)
+        else:
+            ldh = _pitch(t, "h", (X.dtype,), dev, (T, d))
+        h = t.data_ptr()
+    if want_codes:
+        q, ldq, s, n = _token_outputs(o, T, d, dev, want_sums)
+    if y_dtype is not None:
+        t, ldy = o.get("y"), d
+        if t is None:
+            t = o["y"] = torch.empty((T, d), dtype=y_dtype, device=dev)
+        else:
+            ldy = _pitch(t, "y", (y_dtype,), dev, (T, d))
+        y = t.data_ptr()
+    _check("pwq_rms_norm_quantize", _on(
+        X, lib().pwq_rms_norm_quantize, X.data_ptr(), _CODES[X.dtype], T, d, ldx, r, ldr, g,
+        PWQ_F32 if gain is None else _CODES[gain.dtype], eps, h, ldh, q, ldq, s, n, y,
+        PWQ_F32 if y_dtype is None else _CODES.get(y_dtype, -1), ldy))
     return o
 
 
@@ -563,32 +599,39 @@ def quantized_matmul_int8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.
     quantize_tokens or rms_norm_quantize; codes, scales (and zeros) from the RTN or GPTQ calls
     with group_size 0 (int8 codes, or uint8 codes with zeros)."""
     dev = X.device
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
     ldx = _pitch(X, "X", (torch.int8,), dev)
     T, d_in = X.shape
-    if codes.dim() != 2 or codes.shape[1] != d_in:
-        raise ValueError(f"codes: expected d_out x {d_in}")
-    d_out = codes.shape[0]
-    if codes.dtype != (torch.int8 if zeros is None else torch.uint8) or codes.device != dev or not codes.is_contiguous():
-        raise ValueError(f"codes: expected contiguous int8 (uint8 with zeros) on {dev}")
-    _vec(x_scales, "x_scales", (torch.float32,), dev, T)
-    _vec(scales, "scales", (torch.float16,), dev, d_out)
+    sh = codes.shape
+    if (len(sh) != 2 or sh[1] != d_in or codes.dtype != (torch.int8 if zeros is None else torch.uint8) or
+            codes.device != dev or not codes.is_contiguous()):
+        _bad("codes", f"contiguous d_out x {d_in} int8 (uint8 with zeros) on {dev}")
+    m = sh[0]
+    sx, sw = _vec(x_scales, "x_scales", (torch.float32,), dev, T), _vec(scales, "scales", (torch.float16,), dev, m)
+    z = n = w = None
     if zeros is not None:
-        _vec(zeros, "zeros", (torch.int16,), dev, d_out)
+        z = _vec(zeros, "zeros", (torch.int16,), dev, m)
         if x_sums is None:
-            raise ValueError("x_sums: needed with zeros")
-        _vec(x_sums, "x_sums", (torch.int32,), dev, T)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((T, d_out), dtype=out_dtype, device=dev)
-        ldy = _pitch(out, "out", _FLOATS, dev, (T, d_out))
-        nb = lib().pwq_quantized_matmul_int8_workspace_size(T, d_in, d_out)
-        if nb and (ws is None or ws.numel() * ws.element_size() < nb):
+            _bad("x_sums", "the token sums, with zeros")
+        n = _vec(x_sums, "x_sums", (torch.int32,), dev, T)
+    ldy = m
+    if out is None:
+        out = torch.empty((T, m), dtype=out_dtype, device=dev)
+    else:
+        ldy = _pitch(out, "out", _CODES, dev, (T, m))
+    L = lib()
+    nb = L.pwq_quantized_matmul_int8_workspace_size(T, d_in, m)
+    if nb:
+        if ws is None:
             ws = _ws(nb, dev)
-        if nb and (ws.device != dev or not ws.is_contiguous()):
-            raise ValueError(f"ws: expected contiguous bytes on {dev}")
-        _check("pwq_quantized_matmul_int8", lib().pwq_quantized_matmul_int8(
-            _p(X), T, d_in, ldx, _p(x_scales), _p(x_sums) if zeros is not None else None, _p(codes), _p(scales), _p(zeros),
-            d_out, _p(out), _dtype_code(out), ldy, _p(ws) if nb else None, nb, _stream(X)))
+        elif ws.device != dev or not ws.is_contiguous():
+            _bad("ws", f"contiguous bytes on {dev}")
+        w = ws.data_ptr()
+        nb = ws.numel() * ws.element_size()
+    _check("pwq_quantized_matmul_int8", _on(
+        X, L.pwq_quantized_matmul_int8, X.data_ptr(), T, d_in, ldx, sx, n, codes.data_ptr(), sw, z, m, out.data_ptr(),
+        _CODES.get(out.dtype, -1), ldy, w, nb))
     return out
 
 
