@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpwq.so")
 
 SOURCES = ["hessian.hip", "chol.hip", "gptq.hip", "rtn.hip", "mse.hip", "w4a16.hip", "awq.hip",
-           "tokens.hip", "w8a8.hip", "pwq_api.hip"]
+           "tokens.hip", "rmsnorm.hip", "w8a8.hip", "pwq_api.hip"]
 ARCH = os.environ.get("PWQ_OFFLOAD_ARCH", "gfx950")
 CFLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -207,6 +207,73 @@ def test_rms_norm_special_rows(pwq):
     assert torch.isnan(r["scales"]).all().item() and not r["codes"].any().item()
 
 
+@pytest.mark.parametrize("d", [72, 1003, 2048, 8192, 12000, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("place", ["new", "x", "residual", "none"])
+def test_rms_norm_rows_past_float32_products(pwq, d, dtype, place):
+    """16-bit rows whose products with the gain leave float32 or its precise range (tiny, huge, mixed,
+    zero, not finite), among ordinary ones, with h new, in place or not wanted."""
+    rng = np.random.default_rng(d)
+    T = 9
+    tiny, huge = (1e-30, 1e30) if dtype == "bf16" else (6e-8, 3e4)
+    x = rng.standard_normal((T, d)).astype(np.float32)
+    x[1] *= tiny
+    x[2] = np.clip(x[2] * huge, -3e38 if dtype == "bf16" else -6e4, 3e38 if dtype == "bf16" else 6e4)
+    x[3] = 0
+    x[4, d // 2] = np.nan
+    x[5, d - 1] = np.inf
+    x[6, : d // 2] *= tiny
+    x[7] = 0
+    x[7, 3] = tiny
+    X = torch.from_numpy(x).to(TYPES[dtype]).to(DEV)
+    R = torch.zeros_like(X)
+    R[8] = X[0]
+    g = rng.standard_normal(d).astype(np.float32)
+    g[:5] *= 1e-20 if dtype == "bf16" else 1e-5
+    g[5:8] *= 1e20 if dtype == "bf16" else 1e3
+    G = torch.from_numpy(g).to(TYPES[dtype]).to(DEV)
+    h = (X.float() + R.float()).to(X.dtype)
+    y = O.rms_norm(f64(h), f64(G), 1e-30)
+    want = O.rms_norm_quantize(f64(h), f64(G), 1e-30)
+    out = {"x": {"h": X}, "residual": {"h": R}}.get(place)
+    if place == "none":
+        r = pwq.rms_norm_quantize(h, G, eps=1e-30, want_sums=True, y_dtype=torch.float32)
+    else:
+        r = pwq.rms_norm_quantize(X, G, residual=R, eps=1e-30, want_sums=True, y_dtype=torch.float32, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(torch.nan_to_num(r["h"]), torch.nan_to_num(h))
+        assert out is None or r["h"] is (X if place == "x" else R)
+    assert np.isnan(want[1][4:6]).all() and want[1][3] == 0
+    with np.errstate(invalid="ignore"):
+        check_codes(r, want, exact=False, y=y)
+    got, fin = f64(r["y"]), np.isfinite(y) & (np.abs(y) < 3e38)
+    assert np.all(np.abs(got[fin] - y[fin]) <= np.abs(y[fin]) * 1.001 * 2.0 ** -24 + half_step(y[fin], torch.float32))
+
+
+@pytest.mark.parametrize("T,d", [((1 << 22) + 9, 16), ((1 << 20) + 7, 1040)])
+def test_more_rows_than_workgroups(pwq, T, d):
+    """Rows that a workgroup takes after its first: equal to calls on those rows alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(d)
+    X = torch.randn(T, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    G = torch.randn(d, generator=g, device=DEV, dtype=torch.bfloat16)
+    few = torch.cat([torch.arange(64), torch.arange((1 << 20) - 5, (1 << 20) + 7), torch.arange(T - 16, T)]).to(DEV)
+    few = few[few < T]
+    for want_sums in (True, False):
+        r, s = pwq.quantize_tokens(X, want_sums=want_sums), pwq.quantize_tokens(X[few], want_sums=want_sums)
+        assert torch.equal(r["codes"][few], s["codes"]) and torch.equal(r["scales"][few], s["scales"])
+        if want_sums:
+            assert torch.equal(r["sums"][few], s["sums"])
+            assert torch.equal(r["sums"], r["codes"].sum(1, dtype=torch.int32))
+        r, s = pwq.rms_norm_quantize(X, G, want_sums=want_sums), pwq.rms_norm_quantize(X[few], G, want_sums=want_sums)
+        # other thread counts sum the squares in another order: the scale may round to its neighbour
+        assert torch.all((r["scales"][few] - s["scales"]).abs() <= s["scales"] * 2.0 ** -23).item()
+        assert (r["codes"][few].int() - s["codes"].int()).abs().max().item() <= 1
+        assert (r["codes"][few] != s["codes"]).float().mean().item() < 1e-3
+        if want_sums:
+            assert torch.equal(r["sums"], r["codes"].sum(1, dtype=torch.int32))
+
+
 def test_rms_norm_strides(pwq):
     rng = np.random.default_rng(8)
     T, d = 11, 200
