@@ -22,9 +22,8 @@ namespace pwq {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int W8_SPLIT_MIN_K = 512;        // least k of a split
+constexpr int W8_SPLIT_MIN_K = 512;        // least k of a split of the tiles
 
 struct W8Args {
     const int8_t* X;
@@ -39,27 +38,7 @@ struct W8Args {
     int64_t kper;                  // k per split
     int splits, y_dtype;
     int tiles_t, tiles_m;
-    int vec;                       // m and ldy multiples of 4, Y, sw and part aligned for stores of four
 };
-
-__device__ __forceinline__ void w8_store(const W8Args& a, int64_t t, int64_t o, float y) {
-    const int64_t i = t * a.ldy + o;
-    if (a.y_dtype == 0) ((float*)a.Y)[i] = y;
-    else ((uint16_t*)a.Y)[i] = a.y_dtype == 1 ? f32_to_f16_bits(y) : f32_to_bf16_bits(y);
-}
-
-// The sum over k of X (C - z) from the sum over the signed bytes
-__device__ __forceinline__ int w8_sum(const W8Args& a, int acc, int64_t t, int64_t o) {
-    if (!a.zeros) return acc;
-    const int z = a.zeros[o];
-    return (int)((uint32_t)acc + (uint32_t)(128 - (z < 255 ? z : 255)) * (uint32_t)a.sums[t]);
-}
-
-// One output: the scale of the row first (the sum times it stays inside float32's range), the
-// token's last.
-__device__ __forceinline__ float w8_value(const W8Args& a, int acc, int64_t t, int64_t o) {
-    return ((float)w8_sum(a, acc, t, o) * f16_bits_to_f32(a.sw[o])) * a.sx[t];
-}
 
 // What four outputs o .. o + 3, and a token, bring to the result.  Kernels load these before
 // their first store: the compiler has to assume that a store may change them.
@@ -72,27 +51,26 @@ struct W8Tok {
     int sum;
 };
 
+// Four outputs' values are read and written in one piece at any address; the last outputs of a
+// row, where fewer than four are left, one by one.
 __device__ __forceinline__ W8Quad w8_quad(const W8Args& a, int64_t o) {
     W8Quad q;
-    if (a.vec) {
-        o = o < a.m ? o : a.m - 4;                        // m is a multiple of 4 here
-        const uint2 s = *(const uint2*)(a.sw + o);
-        const uint2 z = a.zeros ? *(const uint2*)(a.zeros + o) : make_uint2(0u, 0u);
-        const uint32_t sb[4] = {s.x & 0xffffu, s.x >> 16, s.y & 0xffffu, s.y >> 16};
-        const uint32_t zb[4] = {z.x & 0xffffu, z.x >> 16, z.y & 0xffffu, z.y >> 16};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            q.w[e] = f16_bits_to_f32((uint16_t)sb[e]);
-            q.z[e] = 128 - (int)(zb[e] < 255u ? zb[e] : 255u);
-        }
+    uint16_t s[4], z[4] = {0, 0, 0, 0};
+    if (o + 4 <= a.m) {
+        __builtin_memcpy(s, a.sw + o, 8);
+        if (a.zeros) __builtin_memcpy(z, a.zeros + o, 8);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t i = o + e < a.m ? o + e : a.m - 1;
-            const int z = a.zeros ? a.zeros[i] : 0;
-            q.w[e] = f16_bits_to_f32(a.sw[i]);
-            q.z[e] = 128 - (z < 255 ? z : 255);
+            s[e] = a.sw[i];
+            if (a.zeros) z[e] = a.zeros[i];
         }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        q.w[e] = f16_bits_to_f32(s[e]);
+        q.z[e] = 128 - (z[e] < 255 ? (int)z[e] : 255);
     }
     return q;
 }
@@ -101,18 +79,10 @@ __device__ __forceinline__ W8Tok w8_tok(const W8Args& a, int64_t t) {
     return W8Tok{a.sx[t], a.zeros ? a.sums[t] : 0};
 }
 
-// Outputs o .. o + 3 of token t, or their sums over this split of k
+// Outputs o .. o + 3 of token t from their sums over k.  The scale of the row comes first (the sum
+// times it stays inside float32's range), the token's last.
 template <bool ZP>
-__device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
-    if (o >= a.m || t >= a.T) return;
-    if (a.splits > 1) {
-        int32_t* p = a.part + ((int64_t)blockIdx.y * a.T + t) * a.m + o;
-        if (a.vec) *(i32x4*)p = acc;
-        else
-            for (int e = 0; e < 4; ++e)
-                if (o + e < a.m) p[e] = acc[e];
-        return;
-    }
+__device__ __forceinline__ void w8_put4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
     float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -121,129 +91,46 @@ __device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, i
         asm("" : "+v"(y[e]));                             // rounded to float32 before the conversion, in every kernel
     }
     const int64_t i = t * a.ldy + o;
-    if (a.vec) {
-        // m and ldy multiples of 4, Y aligned: four outputs in one store
-        if (a.y_dtype == 0) {
-            *(float4*)((float*)a.Y + i) = make_float4(y[0], y[1], y[2], y[3]);
-        } else if (a.y_dtype == 1) {
-            *(uint2*)((uint16_t*)a.Y + i) = make_uint2(f32_to_f16_bits(y[0]) | ((uint32_t)f32_to_f16_bits(y[1]) << 16),
-                                                      f32_to_f16_bits(y[2]) | ((uint32_t)f32_to_f16_bits(y[3]) << 16));
+    if (a.y_dtype == 0) {
+        float* p = (float*)a.Y + i;
+        if (o + 4 <= a.m) {
+            __builtin_memcpy(p, y, 16);
         } else {
-            *(uint2*)((uint16_t*)a.Y + i) = make_uint2(f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16),
-                                                      f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16));
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (o + e < a.m) p[e] = y[e];
         }
     } else {
-        for (int e = 0; e < 4; ++e)
-            if (o + e < a.m) w8_store(a, t, o + e, y[e]);
-    }
-}
-
-// ------------------------------------------------------------------ any alignment
-// 128 x 128 tile, four waves of 64 x 64, 64 k per step, operands through registers into LDS:
-// rows may start at any byte and have any length.  A chunk that passes the end of a row is
-// assembled from its bytes with 0 past the end (X's zeros make C's bytes there irrelevant).
-constexpr int G_TILE = 128, G_BK = 64;
-
-// LDS byte offset of row r's 16-byte chunk c
-__device__ __forceinline__ int g_off(int r, int c) { return r * G_BK + 16 * (c ^ ((r >> 1) & 3)); }
-
-__device__ __forceinline__ uint4 g_load(const uint8_t* row, int64_t k, int64_t kend) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (k + 16 <= kend) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
-        uint8_t b[16];
+        uint16_t* p = (uint16_t*)a.Y + i;
+        uint16_t v[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) b[e] = k + e < kend ? row[k + e] : (uint8_t)0;
-        __builtin_memcpy(&v, b, 16);
+        for (int e = 0; e < 4; ++e) v[e] = a.y_dtype == 1 ? f32_to_f16_bits(y[e]) : f32_to_bf16_bits(y[e]);
+        if (o + 4 <= a.m) {
+            __builtin_memcpy(p, v, 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (o + e < a.m) p[e] = v[e];
+        }
     }
-    return v;
 }
 
+// The same, or their sums over this split of k
 template <bool ZP>
-__global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][2 * G_TILE * G_BK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave & 1, wn = wave >> 1;
-    const int64_t t0 = (int64_t)(blockIdx.x % a.tiles_t) * G_TILE;
-    const int64_t o0 = (int64_t)(blockIdx.x / a.tiles_t) * G_TILE;
-    const int64_t kbeg = (int64_t)blockIdx.y * a.kper;
-    const int64_t kend = kbeg + a.kper < a.n ? kbeg + a.kper : a.n;
-
-    // thread t copies the chunk t % 4 of rows t / 4 and 64 + t / 4 of both tiles; rows past the
-    // matrices repeat the last one (their outputs are not stored)
-    const uint8_t* xr[2];
-    const uint8_t* cr[2];
+__device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
+    if (o >= a.m || t >= a.T) return;
+    if (a.splits > 1) {
+        int32_t* p = a.part + ((int64_t)blockIdx.y * a.T + t) * a.m + o;
+        if (o + 4 <= a.m) {
+            __builtin_memcpy(p, &acc, 16);
+        } else {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int64_t r = 64 * q + (tid >> 2);
-        xr[q] = (const uint8_t*)a.X + (t0 + r < a.T ? t0 + r : a.T - 1) * a.ldx;
-        cr[q] = a.C + (o0 + r < a.m ? o0 + r : a.m - 1) * a.n;
+            for (int e = 0; e < 3; ++e)
+                if (o + e < a.m) p[e] = acc[e];
+        }
+        return;
     }
-    uint4 xv[2], cv[2];
-    auto fetch = [&](int64_t k0) {
-        const int64_t k = k0 + 16 * (tid & 3);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            xv[q] = g_load(xr[q], k, kend);
-            cv[q] = g_load(cr[q], k, kend);
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int o = g_off(64 * q + (tid >> 2), tid & 3);
-            *(uint4*)(lds[buf] + o) = xv[q];
-            uint4 c = cv[q];
-            if (ZP) { c.x ^= 0x80808080u; c.y ^= 0x80808080u; c.z ^= 0x80808080u; c.w ^= 0x80808080u; }
-            *(uint4*)(lds[buf] + G_TILE * G_BK + o) = c;
-        }
-    };
-    i32x16 acc[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-    fetch(kbeg);
-    int buf = 0;
-    for (int64_t k0 = kbeg; k0 < kend; k0 += G_BK, buf ^= 1) {
-        // the other buffer's readers passed the barrier of the step before
-        put(buf);
-        __syncthreads();
-        if (k0 + G_BK < kend) fetch(k0 + G_BK);
-        const uint8_t* A = lds[buf];
-        const uint8_t* B = A + G_TILE * G_BK;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            i32x4 fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fa[i] = *(const i32x4*)(A + g_off(wm * 64 + 32 * i + (lane & 31), 2 * ks + (lane >> 5)));
-                fb[i] = *(const i32x4*)(B + g_off(wn * 64 + 32 * i + (lane & 31), 2 * ks + (lane >> 5)));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t o = o0 + wn * 64 + 32 * j + (lane & 31);
-            if (o >= a.m) continue;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int64_t t = t0 + wm * 64 + 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                if (t >= a.T) continue;
-                if (a.splits > 1) a.part[((int64_t)blockIdx.y * a.T + t) * a.m + o] = acc[i][j][v];
-                else w8_store(a, t, o, w8_value(a, acc[i][j][v], t, o));
-            }
-        }
+    w8_put4<ZP>(a, acc, t, o, q, k);
 }
 
 // ------------------------------------------------------------------ rows of 16-byte multiples
@@ -496,6 +383,138 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
         for (int i = 0; i < FH; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
 }
 
+// ------------------------------------------------------------------ any alignment
+// GT x GT tile, four waves as 2 x 2, 128 k per step: rows may start at any byte and have any
+// length.  Operands travel through registers (16-byte loads at any address) into the same LDS
+// layout as the tiles above, P steps ahead of their use; LDS has two buffers and a step one
+// barrier.  The loop has no branch around a load (past the last whole step it loads that one
+// again), so that the wait for one step's loads leaves the later steps' in flight.  The rest of
+// the rows is assembled from its bytes with 0 past the end (X's zeros make the codes' bytes
+// there irrelevant).
+
+// 16 bytes of a row from k on, with 0 past kend (kend >= 1): the 16 that end at kend, moved down
+__device__ __forceinline__ uint4 w8_bytes(const uint8_t* row, int64_t k, int64_t kend) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (kend >= 16) {
+        const int64_t at = k < kend - 16 ? k : kend - 16;
+        __builtin_memcpy(w, row + at, 16);
+        const int by = k - at < 16 ? (int)(k - at) : 16;  // bytes to move down
+#pragma unroll
+        for (int b = 1; b <= 4; b *= 2) {                 // whole words
+            if ((by >> 2) & b) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = c + b < 4 ? w[(c + b) & 3] : 0u;
+            }
+        }
+        const uint32_t rest = (uint32_t)by & 3u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = __builtin_amdgcn_alignbyte(c < 3 ? w[c + 1] : 0u, w[c], rest);
+    } else {
+        for (int e = 0; e < 16; ++e) {
+            if (k + e >= kend) break;
+            const uint32_t byte = (uint32_t)row[k + e] << (8 * (e & 3));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] |= c == e / 4 ? byte : 0u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int GT, int P, bool ZP>
+__global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
+    constexpr int BK = 128, F = GT / 32, NC = GT * 2 * 8 / 256;       // fragments per wave side, chunks per thread
+    constexpr int ST = 2 * GT * BK;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * ST];
+    int to, tt;
+    w8_map(a, blockIdx.x, to, tt);
+    const int64_t o0 = (int64_t)to * GT, t0 = (int64_t)tt * GT;
+    const int64_t kbeg = (int64_t)blockIdx.y * a.kper;
+    const int64_t kend = kbeg + a.kper < a.n ? kbeg + a.kper : a.n;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wo = wave & 1, wt = wave >> 1;
+
+    // chunk j of this thread: chunk tid % 8 of row j 32 + tid / 8 of the codes' GT rows followed by
+    // the activations' GT; rows past the matrices repeat the last one (not stored)
+    const uint8_t* src[NC];
+    int dst[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const int r = j * 32 + (tid >> 3);
+        if (r < GT) src[j] = a.C + (o0 + r < a.m ? o0 + r : a.m - 1) * a.n;
+        else src[j] = (const uint8_t*)a.X + (t0 + r - GT < a.T ? t0 + r - GT : a.T - 1) * a.ldx;
+        dst[j] = r * BK + 16 * w8_pos<BK>(r & 15, tid & 7);
+    }
+    const int nfull = (int)((kend - kbeg) / BK);
+    auto fetch = [&](uint4 (&v)[NC], int it) {
+        const int64_t k = kbeg + (int64_t)(it < nfull ? it : nfull - 1) * BK + 16 * (tid & 7);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) __builtin_memcpy(&v[j], src[j] + k, 16);
+    };
+    i32x4 acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+    const int r = lane & 15, c = lane >> 4;
+    auto step = [&](uint4 (&v)[NC], int buf, int next) {
+        uint8_t* S = lds + buf * ST;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            uint4 w = v[j];
+            if (ZP && j < NC / 2) { w.x ^= 0x80808080u; w.y ^= 0x80808080u; w.z ^= 0x80808080u; w.w ^= 0x80808080u; }
+            *(uint4*)(S + dst[j]) = w;
+        }
+        if (next >= 0) fetch(v, next);
+        w8_wait_lds();
+        w8_barrier();
+#pragma unroll
+        for (int ks = 0; ks < BK / 64; ++ks) {
+            const int o = r * BK + 16 * w8_pos<BK>(r, 4 * ks + c);
+            i32x4 fo[F], ft[F];
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                fo[i] = *(const i32x4*)(S + (wo * (GT / 2) + 16 * i) * BK + o);
+                ft[i] = *(const i32x4*)(S + (GT + wt * (GT / 2) + 16 * i) * BK + o);
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int j = 0; j < F; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fo[i], ft[j], acc[i][j], 0, 0, 0);
+        }
+    };
+    uint4 v[P][NC];
+    int it = 0;
+    if (nfull > 0) {
+#pragma unroll
+        for (int u = 0; u < P; ++u) fetch(v[u], u);
+        for (; it + P <= nfull; it += P) {
+#pragma unroll
+            for (int u = 0; u < P; ++u) step(v[u], u & 1, it + u + P);
+        }
+#pragma unroll
+        for (int u = 0; u < P - 1; ++u)
+            if (it + u < nfull) step(v[u], u & 1, -1);
+    }
+    if (kbeg + (int64_t)nfull * BK < kend) {
+        const int64_t k = kbeg + (int64_t)nfull * BK + 16 * (tid & 7);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[0][j] = w8_bytes(src[j], k, kend);
+        step(v[0], nfull & 1, -1);
+    }
+    W8Quad q[F];
+    W8Tok tok[F];
+    const int64_t ob = o0 + wo * (GT / 2) + 4 * c, tb = t0 + wt * (GT / 2) + r;
+#pragma unroll
+    for (int i = 0; i < F; ++i) q[i] = w8_quad(a, ob + 16 * i);
+#pragma unroll
+    for (int j = 0; j < F; ++j) tok[j] = w8_tok(a, tb + 16 * j);
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int i = 0; i < F; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
+}
+
 // ------------------------------------------------------------------ few tokens
 // Few tokens by short rows, where a launch's latency counts, and one token, where the codes are the
 // traffic: a workgroup owns 16 output rows by 16 tokens, its eight waves share k in turns of
@@ -565,24 +584,41 @@ __global__ __launch_bounds__(512) void w8_row_kernel(W8Args a) {
     w8_out4<ZP>(a, acc, t, o0 + 4 * c, q, tok);
 }
 
-// the splits' sums of each output, scaled
+// ------------------------------------------------------------------ splits
+// The splits' sums of four outputs of a token at a time, scaled.  grid: x = outputs, y = tokens
+template <bool ZP>
 __global__ __launch_bounds__(256) void w8_join_kernel(W8Args a) {
+    const int64_t o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (o >= a.m) return;
+    const W8Quad q = w8_quad(a, o);
     const int64_t size = a.T * a.m;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
-        uint32_t s = 0;
-        for (int k = 0; k < a.splits; ++k) s += (uint32_t)a.part[k * size + i];
-        const int64_t t = i / a.m, o = i - t * a.m;
-        w8_store(a, t, o, w8_value(a, (int)s, t, o));
+    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+        const W8Tok tok = w8_tok(a, t);
+        const int32_t* p = a.part + t * a.m + o;
+        i32x4 s = {0, 0, 0, 0};
+        if (o + 4 <= a.m) {
+            for (int k = 0; k < a.splits; ++k) {
+                i32x4 v;
+                __builtin_memcpy(&v, p + k * size, 16);
+                s += v;
+            }
+        } else {
+            for (int k = 0; k < a.splits; ++k)
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (o + e < a.m) s[e] += p[k * size + e];
+        }
+        w8_put4<ZP>(a, s, t, o, q, tok);
     }
 }
 
 // ------------------------------------------------------------------ which kernel
 struct W8Plan {
-    int kind;                      // W8_ANY, W8_ROW2, W8_ROW4 or an index into w8_tiles
+    int kind;                      // one of the below, or an index into w8_tiles
     int splits;
     int64_t kper;
 };
-constexpr int W8_ANY = -1, W8_ROW2 = -2, W8_ROW4 = -3;
+constexpr int W8_ANY64 = -1, W8_ANY128 = -2, W8_ROW2 = -3, W8_ROW4 = -4;
 
 // k over `s` splits in whole steps of `step`
 W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
@@ -590,13 +626,15 @@ W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
     return W8Plan{kind, (int)cdiv(n, kper), kper};
 }
 
-// Any alignment: splits of k until about two workgroups per compute unit run, each with at least
-// W8_SPLIT_MIN_K.
+// Any alignment: tiles of 64 x 64 while there are few (a split of k would pay another launch), of
+// 128 x 128 from 1024 of those on.
 W8Plan w8_plan_any(int64_t T, int64_t n, int64_t m) {
-    const int64_t tiles = cdiv(T, G_TILE) * cdiv(m, G_TILE);
-    int64_t s = cdiv(512, tiles);
-    if (s > n / W8_SPLIT_MIN_K) s = n / W8_SPLIT_MIN_K;
-    return w8_split(W8_ANY, n, s, G_BK);
+    const int64_t big = cdiv(T, 128) * cdiv(m, 128);
+    if (big >= 1024) return w8_split(W8_ANY128, n, 1, 128);
+    const int64_t tiles = cdiv(T, 64) * cdiv(m, 64);
+    int64_t s = 256 / tiles;
+    if (s > n / 2048) s = n / 2048;
+    return w8_split(W8_ANY64, n, s, 128);
 }
 
 // The tiles, and what one costs on this chip: every compute unit holds one workgroup, which takes
@@ -626,7 +664,7 @@ constexpr int W8_TILES = sizeof(w8_tiles) / sizeof(w8_tiles[0]);
 W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
     const double bytes = ((double)T * n + (double)m * n + 2.0 * T * m) * 1e-6;          // MB
     const double mem = bytes / 5.4 + 2.0;
-    W8Plan best{W8_ANY, 1, n};
+    W8Plan best{0, 1, n};
     double least = 1e30;
     for (int i = 0; i < W8_TILES; ++i) {
         const W8TileCost& c = w8_tiles[i];
@@ -670,12 +708,13 @@ hipError_t w8_row_go(const W8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int GT, int P>
 hipError_t w8_any_go(W8Args a, hipStream_t s) {
-    a.tiles_m = (int)cdiv(a.m, G_TILE);
-    a.tiles_t = (int)cdiv(a.T, G_TILE);
+    a.tiles_m = (int)cdiv(a.m, GT);
+    a.tiles_t = (int)cdiv(a.T, GT);
     const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
-    if (a.zeros) hipLaunchKernelGGL(w8_any_kernel<true>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(w8_any_kernel<false>, grid, dim3(256), 0, s, a);
+    if (a.zeros) hipLaunchKernelGGL((w8_any_kernel<GT, P, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((w8_any_kernel<GT, P, false>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -691,11 +730,13 @@ hipError_t w8_run(W8Args a, const W8Plan& p, hipStream_t s) {
         case 4: e = w8_tile_go<64, 64, 128, 4, 2, 2>(a, s); break;
         case W8_ROW2: e = w8_row_go<2>(a, s); break;
         case W8_ROW4: e = w8_row_go<4>(a, s); break;
-        default: e = w8_any_go(a, s); break;
+        case W8_ANY64: e = w8_any_go<64, 4>(a, s); break;
+        default: e = w8_any_go<128, 2>(a, s); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t blocks = cdiv(a.T * a.m, 256);
-    hipLaunchKernelGGL(w8_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)cdiv(a.m, 1024), (unsigned)(a.T < 32768 ? a.T : 32768));
+    if (a.zeros) hipLaunchKernelGGL(w8_join_kernel<true>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(w8_join_kernel<false>, grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -720,7 +761,6 @@ hipError_t w8_launch(const int8_t* X, int64_t T, int64_t n, int64_t ldx, const f
     W8Args a{};
     a.X = X; a.sx = sx; a.sums = sums; a.C = C; a.sw = sw; a.zeros = zeros; a.Y = Y; a.part = (int32_t*)ws;
     a.ldx = ldx; a.ldy = ldy; a.T = T; a.n = n; a.m = m; a.y_dtype = y_dtype;
-    a.vec = m % 4 == 0 && ldy % 4 == 0 && aligned(Y, y_dtype == 0 ? 16 : 8) && aligned(sw, 8) && aligned(zeros, 8);
     const bool rows16 = n % 16 == 0 && ldx % 16 == 0 && aligned(X, 16) && aligned(C, 16);
     return w8_run(a, rows16 ? w8_plan_fast(T, n, m) : w8_plan_any(T, n, m), s);
 }
