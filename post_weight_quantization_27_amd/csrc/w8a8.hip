@@ -82,14 +82,23 @@ __device__ __forceinline__ W8Tok w8_tok(const W8Args& a, int64_t t) {
 // Outputs o .. o + 3 of token t from their sums over k.  The scale of the row comes first (the sum
 // times it stays inside float32's range), the token's last.
 template <bool ZP>
-__device__ __forceinline__ void w8_put4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
-    float y[4];
+__device__ __forceinline__ void w8_value4(float (&y)[4], i32x4 acc, const W8Quad& q, const W8Tok& k) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int s = ZP ? (int)((uint32_t)acc[e] + (uint32_t)q.z[e] * (uint32_t)k.sum) : acc[e];
         y[e] = ((float)s * q.w[e]) * k.s;
         asm("" : "+v"(y[e]));                             // rounded to float32 before the conversion, in every kernel
     }
+}
+__device__ __forceinline__ uint32_t w8_pair(const W8Args& a, float lo, float hi) {
+    return a.y_dtype == 1 ? (uint32_t)f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16)
+                          : (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+}
+
+template <bool ZP>
+__device__ __forceinline__ void w8_put4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
+    float y[4];
+    w8_value4<ZP>(y, acc, q, k);
     const int64_t i = t * a.ldy + o;
     if (a.y_dtype == 0) {
         float* p = (float*)a.Y + i;
@@ -115,7 +124,38 @@ __device__ __forceinline__ void w8_put4(const W8Args& a, i32x4 acc, int64_t t, i
     }
 }
 
-// The same, or their sums over this split of k
+// Two fragments' outputs in 16 bits, o0 .. o0 + 31 of the 16 tokens that a wave's lanes hold (lane
+// row c: outputs 4 c .. 4 c + 3 of each fragment).  Two swaps between lane rows give row c the
+// outputs 8 c .. 8 c + 7, so that a store writes 64 bytes of a row in one piece instead of 32.
+template <bool ZP>
+__device__ __forceinline__ void w8_put_pair16(const W8Args& a, i32x4 acc0, i32x4 acc1, int64_t t, int64_t o0, int c,
+                                              const W8Quad& q0, const W8Quad& q1, const W8Tok& k) {
+    float y0[4], y1[4];
+    w8_value4<ZP>(y0, acc0, q0, k);
+    w8_value4<ZP>(y1, acc1, q1, k);
+    uint32_t even[2], odd[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const auto s = __builtin_amdgcn_permlane32_swap(w8_pair(a, y0[2 * h], y0[2 * h + 1]),
+                                                        w8_pair(a, y1[2 * h], y1[2 * h + 1]), false, false);
+        const auto r = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+        even[h] = r[0];
+        odd[h] = r[1];
+    }
+    const uint32_t v[4] = {even[0], even[1], odd[0], odd[1]};
+    const int64_t o = o0 + 8 * c;
+    if (o >= a.m || t >= a.T) return;
+    uint16_t* p = (uint16_t*)a.Y + t * a.ldy + o;
+    if (o + 8 <= a.m) {
+        __builtin_memcpy(p, v, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (o + e < a.m) p[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+    }
+}
+
+// Four outputs, or their sums over this split of k
 template <bool ZP>
 __device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, int64_t o, const W8Quad& q, const W8Tok& k) {
     if (o >= a.m || t >= a.T) return;
@@ -377,6 +417,16 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
     for (int i = 0; i < FH; ++i) q[i] = w8_quad(a, ob + 16 * i);
 #pragma unroll
     for (int j = 0; j < FT; ++j) tok[j] = w8_tok(a, tb + 16 * j);
+    if constexpr (FH % 2 == 0) {
+        if (a.splits == 1 && a.y_dtype != 0) {
+#pragma unroll
+            for (int j = 0; j < FT; ++j)
+#pragma unroll
+                for (int i = 0; i < FH; i += 2)
+                    w8_put_pair16<ZP>(a, acc[i][j], acc[i + 1][j], tb + 16 * j, ob - 4 * c + 16 * i, c, q[i], q[i + 1], tok[j]);
+            return;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < FT; ++j)
 #pragma unroll
