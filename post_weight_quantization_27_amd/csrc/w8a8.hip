@@ -23,6 +23,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int W8_CUS = 256;                // compute units (a multiple of the 8 XCDs)
 constexpr int W8_SPLIT_MIN_K = 512;        // least k of a split of the tiles
 
 struct W8Args {
@@ -230,6 +231,12 @@ __device__ __forceinline__ void w8_map(const W8Args& a, int bid, int& to, int& t
     to = 8 * g + in - tt * rows;
 }
 
+// One workgroup per compute unit that goes through its tiles (3-4 % over a workgroup per tile on
+// 8192 x 8192 x 2048 and 8192^3), where the registers allow it: with 256 x 256 tiles it gains
+// nothing and the zero-point form spills.
+template <int BO, int BT, int KG>
+constexpr bool w8_persist = KG == 1 && BO * BT < 65536;
+
 template <int BO, int BT, int BK, int NST, int WO, int KG, bool ZP>
 __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
     constexpr int NW = 8 / KG, WT = NW / WO;              // waves that share a stage
@@ -237,12 +244,10 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
     constexpr int ROWB = 1024 / BK;                       // rows per copy instruction of a wave
     constexpr int L = (BO + BT) / ROWB / NW;              // copies per wave and stage
     constexpr int ST = (BO + BT) * BK;
+    constexpr bool PERSIST = w8_persist<BO, BT, KG>;
     static_assert(L * NW * ROWB == BO + BT && L * (NST - 2) < 64 && KG * NST * ST <= 163840, "tile");
     static_assert(KG == 1 || (FO % 2 == 0 && 8 * FO / 2 * FT * 1024 <= 2 * NST * ST), "the groups' sums fit the stages");
     __shared__ __attribute__((aligned(16))) uint8_t smem[KG * NST * ST];
-    int to, tt;
-    w8_map(a, blockIdx.x, to, tt);
-    const int64_t o0 = (int64_t)to * BO, t0 = (int64_t)tt * BT;
     const int lane = threadIdx.x & 63, wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = KG == 2 ? wave8 & 3 : wave8, grp = wave8 >> 2;
     const int wo = wave / WT, wt = wave % WT;
@@ -262,26 +267,34 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
     const uint8_t* src[L];
     bool is_x[L];
     int chunk[L];
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const int r = (wave * L + j) * ROWB + lane / (BK / 16);
-        chunk[j] = w8_pos<BK>(r & 15, lane % (BK / 16));  // the xor undoes itself
-        is_x[j] = (wave * L + j) * ROWB >= BO;
-        if (is_x[j]) {
-            const int64_t t = t0 + r - BO;
-            src[j] = (const uint8_t*)a.X + (t < a.T ? t : a.T - 1) * a.ldx + kbeg + 16 * chunk[j];
-        } else {
-            const int64_t o = o0 + r;
-            src[j] = a.C + (o < a.m ? o : a.m - 1) * a.n + kbeg + 16 * chunk[j];
-        }
-    }
+    int64_t o0, t0;
     // The order of k is free, so tiles that live on the codes' traffic start at different k:
     // where d_in is a multiple of 4096, rows that are read at the same k in step all come
     // from the same few memory channels (one token by 8192 x 28672 outputs: 52 us without, 44
     // with; at 8320 inputs 43 either way).  Large token tiles share X by k instead and start
     // together.
     constexpr int ROT = BT <= 128 ? 3 : 0;
-    const int rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
+    int rot;
+    auto setup = [&](int tile) {
+        int to, tt;
+        w8_map(a, tile, to, tt);
+        o0 = (int64_t)to * BO;
+        t0 = (int64_t)tt * BT;
+        rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int r = (wave * L + j) * ROWB + lane / (BK / 16);
+            chunk[j] = w8_pos<BK>(r & 15, lane % (BK / 16));      // the xor undoes itself
+            is_x[j] = (wave * L + j) * ROWB >= BO;
+            if (is_x[j]) {
+                const int64_t t = t0 + r - BO;
+                src[j] = (const uint8_t*)a.X + (t < a.T ? t : a.T - 1) * a.ldx + kbeg + 16 * chunk[j];
+            } else {
+                const int64_t o = o0 + r;
+                src[j] = a.C + (o < a.m ? o : a.m - 1) * a.n + kbeg + 16 * chunk[j];
+            }
+        }
+    };
     auto copy = [&](int it) {
         uint8_t* S = lds + (it % NST) * ST + wave * (L * 1024);
         const int pos = it + rot;
@@ -302,21 +315,16 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
         }
     };
 
-    i32x4 acc[FO][FT];
+    // the first NST - 1 stages of a tile
+    auto begin = [&] {
 #pragma unroll
-    for (int i = 0; i < FO; ++i)
-#pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
-#pragma unroll
-    for (int q = 0; q < NST - 1; ++q) {
-        if (q < nfull) copy(q);
-        else if (q < nk) copy_end(q);
-    }
-    if (nk >= NST - 1) w8_wait_vm<L * (NST - 2)>();
-    else w8_wait_vm<0>();
-    w8_barrier();
-    if (grp == 1) w8_barrier();                           // the second group runs half a step behind
+        for (int q = 0; q < NST - 1; ++q) {
+            if (q < nfull) copy(q);
+            else if (q < nk) copy_end(q);
+        }
+    };
 
+    i32x4 acc[FO][FT];
     const int r = lane & 15, c = lane >> 4;
     const uint8_t* la[KS];
     const uint8_t* lb[KS];
@@ -364,73 +372,98 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
         __builtin_amdgcn_sched_barrier(0);
         w8_barrier();
     };
-    int it = 0;
-    for (; it + NST - 1 < nfull; ++it)
-        step(it, [&] {
-            copy(it + NST - 1);
-            __builtin_amdgcn_sched_barrier(0);
-            w8_wait_vm<L * (NST - 2)>();
-        });
-    for (; it < nk; ++it)
-        step(it, [&] {
-            if (it + NST - 1 < nk) copy_end(it + NST - 1);
-            __builtin_amdgcn_sched_barrier(0);
-            w8_wait_vm<0>();
-        });
-    if (KG == 2 && nk < nmax) {                           // the other group's last stage
+    int tile = blockIdx.x;
+    setup(tile);
+    begin();
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FO; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+        if (nk >= NST - 1) w8_wait_vm<L * (NST - 2)>();
+        else w8_wait_vm<0>();
         w8_barrier();
-        w8_barrier();
-    }
-    if (grp == 0) w8_barrier();
+        if (grp == 1) w8_barrier();                           // the second group runs half a step behind
+        int it = 0;
+        for (; it + NST - 1 < nfull; ++it)
+            step(it, [&] {
+                copy(it + NST - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                w8_wait_vm<L * (NST - 2)>();
+            });
+        for (; it < nk; ++it)
+            step(it, [&] {
+                if (it + NST - 1 < nk) copy_end(it + NST - 1);
+                __builtin_amdgcn_sched_barrier(0);
+                w8_wait_vm<0>();
+            });
+        if (KG == 2 && nk < nmax) {                           // the other group's last stage
+            w8_barrier();
+            w8_barrier();
+        }
+        if (grp == 0) w8_barrier();                           // every wave has read its last stage
 
-    // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
-    // second; each takes the other's sums of its half from LDS
-    constexpr int FH = KG == 2 ? FO / 2 : FO;
-    if constexpr (KG == 2) {
-        i32x4* x = (i32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
-        w8_barrier();                                     // every wave has read its last stage
+        // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
+        // second; each takes the other's sums of its half from LDS
+        constexpr int FH = KG == 2 ? FO / 2 : FO;
+        if constexpr (KG == 2) {
+            i32x4* x = (i32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
 #pragma unroll
-        for (int i = 0; i < FH; ++i)
+            for (int i = 0; i < FH; ++i)
 #pragma unroll
-            for (int j = 0; j < FT; ++j) {
-                const i32x4 lo = acc[i][j], hi = acc[FH + i][j];
-                i32x4 send, keep;
+                for (int j = 0; j < FT; ++j) {
+                    const i32x4 lo = acc[i][j], hi = acc[FH + i][j];
+                    i32x4 send, keep;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    send[e] = grp == 0 ? hi[e] : lo[e];
-                    keep[e] = grp == 0 ? lo[e] : hi[e];
+                    for (int e = 0; e < 4; ++e) {
+                        send[e] = grp == 0 ? hi[e] : lo[e];
+                        keep[e] = grp == 0 ? lo[e] : hi[e];
+                    }
+                    x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
+                    acc[i][j] = keep;
                 }
-                x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
-                acc[i][j] = keep;
+            w8_wait_lds();
+            w8_barrier();
+#pragma unroll
+            for (int i = 0; i < FH; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
+        }
+        W8Quad q[FH];
+        W8Tok tok[FT];
+        const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0) + 4 * c, tb = t0 + wt * (BT / WT) + r;
+#pragma unroll
+        for (int i = 0; i < FH; ++i) q[i] = w8_quad(a, ob + 16 * i);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) tok[j] = w8_tok(a, tb + 16 * j);
+        // The next tile's first copies fly while this one's outputs are converted and stored
+        tile += gridDim.x;
+        const bool more = PERSIST && tile < a.tiles_t * a.tiles_m;
+        if (more) {
+            w8_wait_vm<0>();                                  // the scales just loaded, ahead of the copies
+            setup(tile);
+            begin();
+        }
+        bool stored = false;
+        if constexpr (FH % 2 == 0) {
+            if (a.splits == 1 && a.y_dtype != 0) {
+                stored = true;
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+#pragma unroll
+                    for (int i = 0; i < FH; i += 2)
+                        w8_put_pair16<ZP>(a, acc[i][j], acc[i + 1][j], tb + 16 * j, ob - 4 * c + 16 * i, c, q[i],
+                                          q[i + 1], tok[j]);
             }
-        w8_wait_lds();
-        w8_barrier();
-#pragma unroll
-        for (int i = 0; i < FH; ++i)
-#pragma unroll
-            for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
-    }
-    W8Quad q[FH];
-    W8Tok tok[FT];
-    const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0) + 4 * c, tb = t0 + wt * (BT / WT) + r;
-#pragma unroll
-    for (int i = 0; i < FH; ++i) q[i] = w8_quad(a, ob + 16 * i);
-#pragma unroll
-    for (int j = 0; j < FT; ++j) tok[j] = w8_tok(a, tb + 16 * j);
-    if constexpr (FH % 2 == 0) {
-        if (a.splits == 1 && a.y_dtype != 0) {
+        }
+        if (!stored) {
 #pragma unroll
             for (int j = 0; j < FT; ++j)
 #pragma unroll
-                for (int i = 0; i < FH; i += 2)
-                    w8_put_pair16<ZP>(a, acc[i][j], acc[i + 1][j], tb + 16 * j, ob - 4 * c + 16 * i, c, q[i], q[i + 1], tok[j]);
-            return;
+                for (int i = 0; i < FH; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
         }
+        if (!more) break;
     }
-#pragma unroll
-    for (int j = 0; j < FT; ++j)
-#pragma unroll
-        for (int i = 0; i < FH; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
 }
 
 // ------------------------------------------------------------------ any alignment
@@ -688,32 +721,30 @@ W8Plan w8_plan_any(int64_t T, int64_t n, int64_t m) {
 }
 
 // The tiles, and what one costs on this chip: every compute unit holds one workgroup, which takes
-// `fixed` microseconds and `step` more for each 128 k (measured with all 256 at work on 8192 k of
-// weights that come from memory; fewer workgroups save a fifth of a step at most, so rounds of
-// 256 are what counts).
+// `fixed` microseconds and `step` more for each 128 k.
 struct W8TileCost {
     int bo, bt, bk;
     float fixed, step;
 };
 constexpr W8TileCost w8_tiles[] = {
-    {256, 256, 64, 8.f, 1.60f},    // 2.5 POP/s on 8192^3
-    {128, 256, 128, 5.f, 0.85f},
-    {128, 128, 128, 3.f, 0.60f},
-    {128, 64, 128, 2.5f, 0.46f},
-    {64, 64, 128, 2.f, 0.31f},
+    {256, 256, 64, 5.3f, 1.19f},
+    {128, 256, 128, 3.3f, 0.64f},
+    {128, 128, 128, 1.3f, 0.555f},
+    {128, 64, 128, 0.55f, 0.48f},
+    {64, 64, 128, 1.4f, 0.26f},
 };
 constexpr int W8_TILES = sizeof(w8_tiles) / sizeof(w8_tiles[0]);
 
-// The least estimate of: rounds of tiles, over 1 to 8 splits of k whose sums a second launch
-// joins; no less than memory takes for the operands (5.4 TB/s); or one row kernel, whose time is
-// the codes' traffic (5.4 TB/s, once per 16 tokens, and up to 0.45 of it again for X) and the
-// latency of its turns.  Measured over 88 shapes (768 .. 28672 inputs and outputs, 1 .. 2048
-// tokens), the choice is the fastest of the kernels or within 12 % of it; with 128 x 128 tiles
-// alone the same shapes take up to 4 times as long (16 tokens by 28672 inputs: 102 against
-// 45 us; 1 token by 768 x 768: 8 against 3 us).
+// The least estimate (us) of: rounds of tiles on 256 compute units, each a fixed part and its steps
+// of k, over 1 to 8 splits of k whose sums a second launch joins, and no less than memory takes;
+// or the row kernel, whose workgroups stream their 16 rows of codes once per 16 tokens, at 19.5
+// bytes per ns each.  The constants are fitted to the times of every kernel over 544 shapes (512 ..
+// 32000 inputs and outputs, 1 .. 4096 tokens): the choice takes 0.7 % longer than the fastest
+// kernel in the geometric mean and 22 % at the worst (256 tokens by 4096 x 1008: 11.3 against
+// 9.2 us); 128 x 128 tiles alone take 60 % longer in the mean and up to 3.5 times as long.
 W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
     const double bytes = ((double)T * n + (double)m * n + 2.0 * T * m) * 1e-6;          // MB
-    const double mem = bytes / 5.4 + 2.0;
+    const double mem = bytes / 6.8 + 4.9;
     W8Plan best{0, 1, n};
     double least = 1e30;
     for (int i = 0; i < W8_TILES; ++i) {
@@ -724,18 +755,19 @@ W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
             const W8Plan p = w8_split(i, n, s, c.bk);
             if (s > 1 && p.splits < s) continue;
             const double rounds = (double)cdiv(tiles * p.splits, 256);
-            const double work = 2.0 + rounds * (c.fixed + c.step * (double)p.kper / 128.0);
-            double t = (work > mem ? work : mem) + 0.05 * work;
-            if (p.splits > 1) t += 4.0 + 2.0 * (double)p.splits * T * m * 4e-6 / 4.0;
+            const double work = 1.3 + rounds * (c.fixed + c.step * (double)p.kper / 128.0);
+            double t = (work > mem ? work : mem) + 0.001 * work;
+            if (p.splits > 1) t += 2.9 + 0.6 * (double)p.splits * T * m * 4e-6;
             if (t < least) { least = t; best = p; }
         }
     }
     if (T <= 1024) {
-        const double traffic = (double)m * n * 1e-6 * (double)cdiv(T, 16) * (1.0 + 0.45 * (T < 16 ? T : 16) / 16.0) / 5.4;
-        const double t = 2.2 + traffic + 0.2 * (double)cdiv(n, 1024);
-        // turns of 8 waves x 128 k fill the waves of short rows, turns of 256 k keep more loads
-        // in flight on long ones (28672 x 1024: 8.6 against 12 us; 8192 x 8192: 16.1 against 15.8)
-        if (t < least) best = w8_split(n < 4096 ? W8_ROW2 : W8_ROW4, n, 1, 64);
+        const double groups = (double)cdiv(cdiv(m, 16) * cdiv(T, 16), 256);
+        const double one = 16e-3 * (double)n * (1.0 + 0.36 * (T < 16 ? T : 16) / 16.0) / 19.5;
+        const double t = 1.9 + groups * one + 0.12 * (double)cdiv(n, 1024);
+        // turns of 8 waves x 128 k; of 256 k where they come out even on long rows (1 token:
+        // 8192 x 8192 14.8 against 15.7 us, but 5120 x 5120 12.5 against 10.3)
+        if (t < least) best = w8_split(n >= 8192 && n % 2048 == 0 ? W8_ROW4 : W8_ROW2, n, 1, 64);
     }
     return best;
 }
@@ -744,7 +776,8 @@ template <int BO, int BT, int BK, int NST, int WO, int KG>
 hipError_t w8_tile_go(W8Args a, hipStream_t s) {
     a.tiles_m = (int)cdiv(a.m, BO);
     a.tiles_t = (int)cdiv(a.T, BT);
-    const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
+    const int64_t tiles = a.tiles_m * (int64_t)a.tiles_t;
+    const dim3 grid((unsigned)(w8_persist<BO, BT, KG> && tiles > W8_CUS ? W8_CUS : tiles), (unsigned)a.splits);
     if (a.zeros) hipLaunchKernelGGL((w8_tile_kernel<BO, BT, BK, NST, WO, KG, true>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((w8_tile_kernel<BO, BT, BK, NST, WO, KG, false>), grid, dim3(512), 0, s, a);
     return hipGetLastError();
