@@ -468,37 +468,37 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 
 // ------------------------------------------------------------------ any alignment
 // GT x GT tile, four waves as 2 x 2, 128 k per step: rows may start at any byte and have any
-// length.  Operands travel through registers (16-byte loads at any address) into the same LDS
-// layout as the tiles above, P steps ahead of their use; LDS has two buffers and a step one
-// barrier.  The loop has no branch around a load (past the last whole step it loads that one
-// again), so that the wait for one step's loads leaves the later steps' in flight.  The rest of
-// the rows is assembled from its bytes with 0 past the end (X's zeros make the codes' bytes
-// there irrelevant).
+// length.  Operands travel through registers into the same LDS layout as the tiles above, P steps
+// ahead of their use; LDS has two buffers and a step one barrier.  No load stands behind a branch,
+// so that the wait for one step's loads leaves the later steps' in flight.
+//
+// The last step may be partial: each 16 bytes past the end is the row's last 16 instead, moved
+// down in registers, with 0 behind (X's zeros make the codes' bytes there irrelevant), fetched
+// ahead like the others.
+//
+// 333 tokens by 5003 outputs: 10 us with rows of 1664 (whole cache lines; the tiles above), 13.4
+// with 1604 (a chunk of 128 takes two lines), 15.3 with 1602 and 17.3 with 1601 (16 bytes from an
+// odd address take the load path about twice as long; loads of the words around them, moved down
+// by 0 to 3 bytes, are 1 to 5 % faster there and 10 % slower at few tokens, as they are five).
 
-// 16 bytes of a row from k on, with 0 past kend (kend >= 1): the 16 that end at kend, moved down
-__device__ __forceinline__ uint4 w8_bytes(const uint8_t* row, int64_t k, int64_t kend) {
+// The 16 bytes from byte `by` (0 .. 16) on, with 0 behind them
+__device__ __forceinline__ uint4 w8_drop(uint4 v, int by) {
+    if (by & 16) v = make_uint4(0u, 0u, 0u, 0u);
+    if (by & 8) v = make_uint4(v.z, v.w, 0u, 0u);
+    if (by & 4) v = make_uint4(v.y, v.z, v.w, 0u);
+    const uint32_t b = (uint32_t)by & 3u;
+    return make_uint4(__builtin_amdgcn_alignbyte(v.y, v.x, b), __builtin_amdgcn_alignbyte(v.z, v.y, b),
+                      __builtin_amdgcn_alignbyte(v.w, v.z, b), __builtin_amdgcn_alignbyte(0u, v.w, b));
+}
+
+// 16 bytes of a row shorter than 16, from its byte k on, with 0 past its n
+__device__ __forceinline__ uint4 w8_short(const uint8_t* row, int64_t k, int64_t n) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (kend >= 16) {
-        const int64_t at = k < kend - 16 ? k : kend - 16;
-        __builtin_memcpy(w, row + at, 16);
-        const int by = k - at < 16 ? (int)(k - at) : 16;  // bytes to move down
+#pragma unroll 1
+    for (int e = 0; e < 16 && k + e < n; ++e) {
+        const uint32_t byte = (uint32_t)row[k + e] << (8 * (e & 3));
 #pragma unroll
-        for (int b = 1; b <= 4; b *= 2) {                 // whole words
-            if ((by >> 2) & b) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) w[c] = c + b < 4 ? w[(c + b) & 3] : 0u;
-            }
-        }
-        const uint32_t rest = (uint32_t)by & 3u;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = __builtin_amdgcn_alignbyte(c < 3 ? w[c + 1] : 0u, w[c], rest);
-    } else {
-        for (int e = 0; e < 16; ++e) {
-            if (k + e >= kend) break;
-            const uint32_t byte = (uint32_t)row[k + e] << (8 * (e & 3));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) w[c] |= c == e / 4 ? byte : 0u;
-        }
+        for (int c = 0; c < 4; ++c) w[c] |= c == e / 4 ? byte : 0u;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -527,9 +527,13 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
         else src[j] = (const uint8_t*)a.X + (t0 + r - GT < a.T ? t0 + r - GT : a.T - 1) * a.ldx;
         dst[j] = r * BK + 16 * w8_pos<BK>(r & 15, tid & 7);
     }
-    const int nfull = (int)((kend - kbeg) / BK);
+    const int nsteps = (int)cdiv(kend - kbeg, BK), nfull = (int)((kend - kbeg) / BK);
+    auto at = [&](int it) {                                   // the step's k here, no later than the last 16 bytes
+        const int64_t k = kbeg + (int64_t)(it < nsteps ? it : nsteps - 1) * BK + 16 * (tid & 7);
+        return k < kend - 16 ? k : kend - 16;
+    };
     auto fetch = [&](uint4 (&v)[NC], int it) {
-        const int64_t k = kbeg + (int64_t)(it < nfull ? it : nfull - 1) * BK + 16 * (tid & 7);
+        const int64_t k = at(it);
 #pragma unroll
         for (int j = 0; j < NC; ++j) __builtin_memcpy(&v[j], src[j] + k, 16);
     };
@@ -539,15 +543,7 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
 #pragma unroll
         for (int j = 0; j < F; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
     const int r = lane & 15, c = lane >> 4;
-    auto step = [&](uint4 (&v)[NC], int buf, int next) {
-        uint8_t* S = lds + buf * ST;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            uint4 w = v[j];
-            if (ZP && j < NC / 2) { w.x ^= 0x80808080u; w.y ^= 0x80808080u; w.z ^= 0x80808080u; w.w ^= 0x80808080u; }
-            *(uint4*)(S + dst[j]) = w;
-        }
-        if (next >= 0) fetch(v, next);
+    auto multiply = [&](const uint8_t* S) {
         w8_wait_lds();
         w8_barrier();
 #pragma unroll
@@ -566,24 +562,42 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fo[i], ft[j], acc[i][j], 0, 0, 0);
         }
     };
-    uint4 v[P][NC];
-    int it = 0;
-    if (nfull > 0) {
+    auto put = [&](uint8_t* S, int j, uint4 w) {
+        if (ZP && j < NC / 2) { w.x ^= 0x80808080u; w.y ^= 0x80808080u; w.z ^= 0x80808080u; w.w ^= 0x80808080u; }
+        *(uint4*)(S + dst[j]) = w;
+    };
+    // step `it` (a whole one: 128 k), whose chunks are in v; v is refilled for a later one under its
+    // products
+    auto step = [&](uint4 (&v)[NC], int it, int next) {
+        uint8_t* S = lds + (it & 1) * ST;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) put(S, j, v[j]);
+        fetch(v, next);
+        multiply(S);
+    };
+    auto last = [&](uint4 (&v)[NC], int it) {                 // one of the last, nothing to fetch
+        uint8_t* S = lds + (it & 1) * ST;
+        const int64_t drop = kbeg + (int64_t)it * BK + 16 * (tid & 7) - at(it);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) put(S, j, it < nfull ? v[j] : w8_drop(v[j], (int)(drop < 16 ? drop : 16)));
+        multiply(S);
+    };
+    if (a.n >= 16) {
+        uint4 v[P][NC];
 #pragma unroll
         for (int u = 0; u < P; ++u) fetch(v[u], u);
+        int it = 0;
         for (; it + P <= nfull; it += P) {
 #pragma unroll
-            for (int u = 0; u < P; ++u) step(v[u], u & 1, it + u + P);
+            for (int u = 0; u < P; ++u) step(v[u], it + u, it + u + P);
         }
 #pragma unroll
-        for (int u = 0; u < P - 1; ++u)
-            if (it + u < nfull) step(v[u], u & 1, -1);
-    }
-    if (kbeg + (int64_t)nfull * BK < kend) {
-        const int64_t k = kbeg + (int64_t)nfull * BK + 16 * (tid & 7);
+        for (int u = 0; u < P; ++u)
+            if (it + u < nsteps) last(v[u], it + u);
+    } else {                                                  // one step
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[0][j] = w8_bytes(src[j], k, kend);
-        step(v[0], nfull & 1, -1);
+        for (int j = 0; j < NC; ++j) put(lds, j, w8_short(src[j], 16 * (tid & 7), a.n));
+        multiply(lds);
     }
     W8Quad q[F];
     W8Tok tok[F];
