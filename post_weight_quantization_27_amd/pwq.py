@@ -525,11 +525,10 @@ def _token_outputs(o: dict, T: int, d: int, dev, want_sums: bool):
         s = o["scales"] = torch.empty((T,), dtype=torch.float32, device=dev)
     else:
         _vec(s, "scales", (torch.float32,), dev, T)
-    n = None
-    if want_sums:
-        n = o.get("sums")
-        if n is None:
-            n = o["sums"] = torch.empty((T,), dtype=torch.int32, device=dev)
+    n = o.get("sums")
+    if n is None and want_sums:
+        n = o["sums"] = torch.empty((T,), dtype=torch.int32, device=dev)
+    if n is not None:
         n = _vec(n, "sums", (torch.int32,), dev, T)
     return q.data_ptr(), ldq, s.data_ptr(), n
 
@@ -538,7 +537,8 @@ def quantize_tokens(X: torch.Tensor, channel_scale: Optional[torch.Tensor] = Non
                     out: Optional[dict] = None) -> dict:
     """int8 codes of activations with one float32 scale per token: {codes (tokens x d), scales
     (tokens), sums (int32, with want_sums)}.  ``channel_scale`` (float32, d): X is divided by it
-    column-wise first (awq_search's ``s``).  ``out`` may hold tensors to write into."""
+    column-wise first (awq_search's ``s``).  ``out`` may hold tensors to write into (every one of
+    these names that is there is written)."""
     dev = X.device
     if dev.type != "cuda":
         _bad("X", "a GPU tensor")
@@ -557,13 +557,20 @@ def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, resi
     """y = h * gain / sqrt(mean(h^2) + eps) with h = X + residual: {codes, scales, sums (with
     want_sums)} as quantize_tokens gives them for y, h (the sum, in X's type, with a residual;
     ``out={"h": residual}`` updates it in place), y (with ``y_dtype``: y rounded to that type,
-    e.g. the float16 input of quantized_matmul; ``want_codes=False`` for y alone)."""
+    e.g. the float16 input of quantized_matmul; ``want_codes=False`` for y alone).  Every tensor of
+    ``out`` with one of these names is written; none but h may share memory with an input."""
     dev = X.device
     if dev.type != "cuda":
         _bad("X", "a GPU tensor")
     ldx = _pitch(X, "X", _CODES, dev)
     T, d = X.shape
     o = out if out is not None else {}
+    if not want_codes and (want_sums or any(o.get(k) is not None for k in ("codes", "scales", "sums"))):
+        _bad("want_codes", "True, with sums or tensors for them")
+    if residual is None and o.get("h") is not None:
+        _bad("h", "no tensor without a residual")
+    if y_dtype is None and o.get("y") is not None:
+        y_dtype = o["y"].dtype
     g = None if gain is None else _vec(gain, "gain", _CODES, dev, d)
     r = h = q = s = n = y = None
     ldr = ldh = ldq = ldy = 0

@@ -417,6 +417,13 @@ def test_quantized_matmul_int8_large_sampled(pwq, T, n, m, zp, odt):
     assert torch.equal(Y[:few], got)
 
 
+@pytest.mark.parametrize("T,n,m,zp,odt", [(4200, 144, 4100, True, "bf16"), (2100, 400, 9100, False, "f32"),
+                                          (4200, 48, 8300, True, "f16"), (2962, 28672, 2756, True, "f16")])
+def test_quantized_matmul_int8_several_tiles_per_workgroup(pwq, T, n, m, zp, odt):
+    """More tiles than compute units: few steps of k per tile, and a split k on top."""
+    test_quantized_matmul_int8_large_sampled(pwq, T, n, m, zp, odt)
+
+
 def test_quantized_matmul_int8_scales(pwq):
     """Scales at the ends of their ranges: a token of scale 0 or NaN, products that a scale alone
     would carry out of float32's range."""
@@ -487,6 +494,50 @@ def test_refusals(pwq):
         pwq.quantize_tokens(torch.zeros(1, 65536, device=DEV))
     with pytest.raises(pwq.PwqError):
         pwq.rms_norm_quantize(x, eps=-1.0)
+
+
+@pytest.mark.parametrize("n", [256, 250])
+def test_offsets_past_32_bits(pwq, n):
+    """Rows 2^30 elements apart, so that the last starts behind 2^31 elements."""
+    rng = np.random.default_rng(n)
+    T, m, ld = 3, 72, (1 << 30) - (0 if n % 16 == 0 else 3)
+    rows = lambda dtype, w: torch.empty(T * ld, dtype=dtype, device=DEV).view(T, ld)[:, :w]
+    x = torch.from_numpy(rng.standard_normal((T, n))).to(DEV).half()
+    X, H, Q = rows(torch.float16, n), rows(torch.float16, n), rows(torch.int8, n)
+    X.copy_(x)
+    a = pwq.quantize_tokens(X, want_sums=True, out={"codes": Q})
+    check_codes(a, O.quantize_tokens(f64(x)), exact=True)
+    C = torch.from_numpy(rng.integers(-127, 128, (m, n)).astype(np.int8)).to(DEV)
+    sw = torch.from_numpy(rng.random(m) + 0.5).to(DEV).half()
+    want = pwq.quantized_matmul_int8(a["codes"].contiguous(), a["scales"], C, sw, out_dtype=torch.float32)
+    Y = rows(torch.float32, m)
+    got = pwq.quantized_matmul_int8(a["codes"], a["scales"], C, sw, out=Y)
+    assert got is Y and torch.equal(Y, want)
+    b = pwq.rms_norm_quantize(X, residual=X, want_sums=True, out={"codes": Q, "h": H})
+    h = x + x
+    assert torch.equal(H, h)
+    check_codes(b, O.rms_norm_quantize(f64(h), None, 1e-5), exact=False, y=O.rms_norm(f64(h), None, 1e-5))
+
+
+def test_tensors_of_out_are_written_or_refused(pwq):
+    """A dictionary of an earlier call, used again: nothing in it keeps the earlier call's values."""
+    rng = np.random.default_rng(8)
+    X = torch.from_numpy(rng.standard_normal((5, 200))).to(DEV).half()
+    R = torch.from_numpy(rng.standard_normal((5, 200))).to(DEV).half()
+    o = pwq.rms_norm_quantize(X, residual=R, want_sums=True, y_dtype=torch.float32)
+    again = pwq.rms_norm_quantize(R, residual=R, out=o)                       # no want_sums, no y_dtype
+    want = pwq.rms_norm_quantize(R, residual=R, want_sums=True, y_dtype=torch.float32)
+    assert again is o and set(o) == set(want) and all(torch.equal(o[k], want[k]) for k in want)
+    with pytest.raises(ValueError):
+        pwq.rms_norm_quantize(X, out=o)                                       # its h
+    with pytest.raises(ValueError):
+        pwq.rms_norm_quantize(X, y_dtype=torch.float16, want_codes=False, out={"sums": o["sums"]})
+    with pytest.raises(ValueError):
+        pwq.rms_norm_quantize(X, y_dtype=torch.float16, want_codes=False, want_sums=True)
+    q = pwq.quantize_tokens(X, want_sums=True)
+    pwq.quantize_tokens(R, out=q)
+    want = pwq.quantize_tokens(R, want_sums=True)
+    assert all(torch.equal(q[k], want[k]) for k in want)
 
 
 # ------------------------------------------------------------------ together
