@@ -517,17 +517,17 @@ def _token_outputs(o: dict, T: int, d: int, dev, want_sums: bool):
     """(codes, its pitch, scales, sums): addresses in o's tensors, which are made where missing."""
     q, ldq = o.get("codes"), d
     if q is None:
-        q = o["codes"] = torch.empty((T, d), dtype=torch.int8, device=dev)
+        q = o["codes"] = torch.empty(T, d, dtype=torch.int8, device=dev)
     else:
         ldq = _pitch(q, "codes", (torch.int8,), dev, (T, d))
     s = o.get("scales")
     if s is None:
-        s = o["scales"] = torch.empty((T,), dtype=torch.float32, device=dev)
+        s = o["scales"] = torch.empty(T, dtype=torch.float32, device=dev)
     else:
         _vec(s, "scales", (torch.float32,), dev, T)
     n = o.get("sums")
     if n is None and want_sums:
-        n = o["sums"] = torch.empty((T,), dtype=torch.int32, device=dev)
+        n = o["sums"] = torch.empty(T, dtype=torch.int32, device=dev)
     if n is not None:
         n = _vec(n, "sums", (torch.int32,), dev, T)
     return q.data_ptr(), ldq, s.data_ptr(), n
@@ -578,7 +578,7 @@ def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, resi
         ldr = _pitch(residual, "residual", (X.dtype,), dev, (T, d))
         r, t, ldh = residual.data_ptr(), o.get("h"), d
         if t is None:
-            t = o["h"] = torch.empty((T, d), dtype=X.dtype, device=dev)
+            t = o["h"] = torch.empty(T, d, dtype=X.dtype, device=dev)
         else:
             ldh = _pitch(t, "h", (X.dtype,), dev, (T, d))
         h = t.data_ptr()
@@ -587,7 +587,7 @@ def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, resi
     if y_dtype is not None:
         t, ldy = o.get("y"), d
         if t is None:
-            t = o["y"] = torch.empty((T, d), dtype=y_dtype, device=dev)
+            t = o["y"] = torch.empty(T, d, dtype=y_dtype, device=dev)
         else:
             ldy = _pitch(t, "y", (y_dtype,), dev, (T, d))
         y = t.data_ptr()
@@ -624,7 +624,7 @@ def quantized_matmul_int8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.
         n = _vec(x_sums, "x_sums", (torch.int32,), dev, T)
     ldy = m
     if out is None:
-        out = torch.empty((T, m), dtype=out_dtype, device=dev)
+        out = torch.empty(T, m, dtype=out_dtype, device=dev)
     else:
         ldy = _pitch(out, "out", _CODES, dev, (T, m))
     L = lib()
