@@ -22,11 +22,13 @@
 // codes written once: memory bound at 7 bytes per element (16-bit types with a residual) or 3
 // (token quantizer).
 //
-// Layout: NT threads per row (whole waves), NC chunks of 8 consecutive elements per thread.  The
-// launch takes 256 threads (several rows in flight on a compute unit, so that one's loads run
-// beside another's stores) and up to 4 chunks before it takes more threads, and the widest
-// thread count when there are fewer rows than compute units (latency).  Rows too long for the
-// registers are read again for the second step.
+// Layout: NT threads per row (whole waves), NC chunks of 8 consecutive elements per thread: few
+// threads with several chunks, so that a compute unit has several rows in flight and one's loads
+// run beside another's stores.  Rows too long for the registers are read again for the second
+// step.  Measured: norm of 8192 x 8192 bf16 with a residual 92-97 us (4.8-5.1 TB/s, as a copy of
+// as many bytes), rows that start at any byte 122 us; token quantizer of 4096 x 28672 bf16
+// 70-79 us (4.5-5.1 TB/s), with a channel scale 119 us (its division and its loads, which are
+// twice X's); one row of 8192 4.3 us, an empty launch 2.2.
 #pragma once
 
 #include "../../include/pwq.h"
@@ -45,6 +47,10 @@ constexpr int64_t TOK_MAX_BLOCKS = 1 << 20;    // rows past this are taken by a 
 
 // y = x, y = x / c; the norm with float32 products of 16-bit values, with float64 products
 enum { TOK_PLAIN, TOK_CHAN, TOK_NORM16, TOK_NORM64 };
+
+// Rows: 16-byte loads and stores of eight elements at multiples of their size (a width that is a
+// multiple of 8), at any address, and rows shorter than eight elements
+enum { ROWS_VEC, ROWS_ANY, ROWS_SHORT };
 
 struct TokArgs {
     const void* X;
@@ -72,24 +78,21 @@ struct Raw {
     static constexpr int N = XT == 0 ? 8 : 4;
     static constexpr int SIZE = XT == 0 ? 4 : 2;
     uint32_t w[N];
-    // Elements col .. col + 7 of a row of d; zeros past its end.  Unaligned rows (UNAL): the chunk
-    // that passes the end is loaded from d - 8 on and moved down, so that every load is issued
-    // without a branch; rows shorter than a chunk are read element by element.  A chunk wholly
-    // past the end is loaded from somewhere in the row and not used.
-    template <bool UNAL>
-    __device__ __forceinline__ void load(const void* row, int col, int d) {
-        if constexpr (!UNAL) {
+    // Elements col .. col + 7 of a row of d, zeros past its end, in two parts: all of a row's chunks
+    // are fetched before the first is settled, which waits for it.  ROWS_ANY: the chunk that
+    // passes the end is fetched from d - 8 on and moved down.  No load stands behind a branch.  A
+    // chunk wholly past the end is fetched from somewhere in the row and not used.
+    template <int AL>
+    __device__ __forceinline__ void fetch(const void* row, int col, int d) {
+        if constexpr (AL == ROWS_VEC) {
             const uint4* v = (const uint4*)((const char*)row + (int64_t)(col < d ? col : 0) * SIZE);
 #pragma unroll
             for (int c = 0; c < N / 4; ++c) {
                 const uint4 u = v[c];
                 w[4 * c] = u.x; w[4 * c + 1] = u.y; w[4 * c + 2] = u.z; w[4 * c + 3] = u.w;
             }
-        } else if (d >= 8) {
-            const int at = col < d - 8 ? col : d - 8;
-            __builtin_memcpy(w, (const char*)row + (int64_t)at * SIZE, 8 * SIZE);
-            const int by = col - at;
-            if (by > 0) down(by);
+        } else if constexpr (AL == ROWS_ANY) {
+            __builtin_memcpy(w, (const char*)row + (int64_t)(col < d - 8 ? col : d - 8) * SIZE, 8 * SIZE);
         } else {
             zero();
             if (col == 0) {
@@ -100,11 +103,20 @@ struct Raw {
             }
         }
     }
+    template <int AL>
+    __device__ __forceinline__ void settle(int col, int d) {
+        if (AL == ROWS_ANY && col > d - 8 && col < d) down(col - (d - 8));
+    }
+    template <int AL>
+    __device__ __forceinline__ void load(const void* row, int col, int d) {
+        fetch<AL>(row, col, d);
+        settle<AL>(col, d);
+    }
     // Elements col .. min(col + 8, d) - 1 into the row
-    template <bool UNAL>
+    template <int AL>
     __device__ __forceinline__ void store(void* row, int col, int d) const {
         char* p = (char*)row + (int64_t)col * SIZE;
-        if constexpr (!UNAL) {
+        if constexpr (AL == ROWS_VEC) {
 #pragma unroll
             for (int c = 0; c < N / 4; ++c) ((uint4*)p)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         } else if (col + 8 <= d) {
@@ -168,14 +180,14 @@ struct Raw {
 };
 
 // y of eight elements, rounded to y_dtype
-template <bool UNAL>
+template <int AL>
 __device__ __forceinline__ void store_y(const TokArgs& a, int64_t row, int col, const float (&y)[8]) {
     char* p = (char*)a.Y + row * a.ldy * (a.y_dtype == 0 ? 4 : 2);
     if (a.y_dtype == 0) {
         Raw<0> r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.w[e] = __builtin_bit_cast(uint32_t, y[e]);
-        r.template store<UNAL>(p, col, a.d);
+        r.template store<AL>(p, col, a.d);
     } else {
         Raw<1> r;
 #pragma unroll
@@ -184,12 +196,12 @@ __device__ __forceinline__ void store_y(const TokArgs& a, int64_t row, int col, 
             r.w[c] = a.y_dtype == 1 ? (uint32_t)f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16)
                                     : (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
         }
-        r.template store<UNAL>(p, col, a.d);
+        r.template store<AL>(p, col, a.d);
     }
 }
 
 // eight codes, from float64 values whose low byte each is, into the row; returns their sum
-template <bool UNAL>
+template <int AL>
 __device__ __forceinline__ int store_codes(int8_t* q, int col, int d, const double (&v)[8], bool live) {
     uint32_t w[2];
     int sum = 0;
@@ -202,7 +214,7 @@ __device__ __forceinline__ int store_codes(int8_t* q, int col, int d, const doub
         // past the end of a row the values are 0, and so are these codes
         sum = __builtin_amdgcn_sdot4((int)w[k], 0x01010101, sum, false);
     }
-    if constexpr (!UNAL) {
+    if constexpr (AL == ROWS_VEC) {
         *(uint2*)(q + col) = make_uint2(w[0], w[1]);
     } else if (col + 8 <= d) {
         __builtin_memcpy(q + col, w, 8);
@@ -272,7 +284,7 @@ struct TokLds {
 // One row of the norm in float64 products, read from memory in each of its two steps: rows that
 // the float32 products do not cover, and rows too long for the registers.  h_done: h has been
 // written to a.H already (by the same threads, the same elements), and x may be gone with it.
-template <int XT, int NT, bool UNAL>
+template <int XT, int NT, int AL>
 __device__ void norm_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT / WAVE>& lds, bool h_done) {
     const int tid = threadIdx.x % NT;
     constexpr int SIZE = Raw<XT>::SIZE;
@@ -281,17 +293,17 @@ __device__ void norm_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT /
     char* hrow = a.H ? (char*)a.H + row * a.ldh * SIZE : nullptr;
     auto read = [&](int col, Raw<XT>& h, float (&g)[8], bool from_h) {
         if (from_h) {
-            h.template load<UNAL>(hrow, col, a.d);
+            h.template load<AL>(hrow, col, a.d);
         } else {
-            h.template load<UNAL>(xrow, col, a.d);
+            h.template load<AL>(xrow, col, a.d);
             if (rrow) {
                 Raw<XT> r;
-                r.template load<UNAL>(rrow, col, a.d);
+                r.template load<AL>(rrow, col, a.d);
                 h.add(h, r);
             }
         }
         auto gains = [&](auto raw) {
-            raw.template load<UNAL>(a.G, col, a.d);
+            raw.template load<AL>(a.G, col, a.d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = raw.get(e);
         };
@@ -312,7 +324,7 @@ __device__ void norm_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT /
         Raw<XT> h;
         float g[8];
         read(col, h, g, h_done && hrow);
-        if (!h_done && hrow) h.template store<UNAL>(hrow, col, a.d);
+        if (!h_done && hrow) h.template store<AL>(hrow, col, a.d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const double hd = (double)h.get(e), p = hd * (double)g[e];
@@ -340,8 +352,8 @@ __device__ void norm_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT /
             q[e] = fma(p, inv, TOK_RINT);
             y[e] = (float)(p * rstd);
         }
-        if (a.Q) sum += store_codes<UNAL>(a.Q + row * a.ldq, col, a.d, q, s.live);
-        if (a.Y) store_y<UNAL>(a, row, col, y);
+        if (a.Q) sum += store_codes<AL>(a.Q + row * a.ldq, col, a.d, q, s.live);
+        if (a.Y) store_y<AL>(a, row, col, y);
     }
     if (a.sums) {
         sum = row_reduce<NT>(sum, lds.sum[par], [](int x, int y) { return x + y; });
@@ -351,17 +363,17 @@ __device__ void norm_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT /
 
 // One row of the token quantizer, read from memory in each of its two steps: rows too long for the
 // registers.
-template <int XT, int NT, bool UNAL>
+template <int XT, int NT, int AL>
 __device__ void tok_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT / WAVE>& lds) {
     const int tid = threadIdx.x % NT;
     const char* xrow = (const char*)a.X + row * a.ldx * Raw<XT>::SIZE;
     auto read = [&](int col, float (&y)[8]) {
         Raw<XT> x;
-        x.template load<UNAL>(xrow, col, a.d);
+        x.template load<AL>(xrow, col, a.d);
         Raw<0> c;
-        if (a.chan) c.template load<UNAL>(a.chan, col, a.d);
+        if (a.chan) c.template load<AL>(a.chan, col, a.d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = !a.chan || (UNAL && col + e >= a.d) ? x.get(e) : x.get(e) / c.get(e);
+        for (int e = 0; e < 8; ++e) y[e] = !a.chan || (AL != ROWS_VEC && col + e >= a.d) ? x.get(e) : x.get(e) / c.get(e);
     };
     float top = 0.f;
     for (int col = tid * 8; col < a.d; col += NT * 8) {
@@ -381,7 +393,7 @@ __device__ void tok_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT / 
         read(col, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = (fma((double)y[e], inv, TOK_SNAP) - TOK_SNAP) + TOK_RINT;
-        sum += store_codes<UNAL>(a.Q + row * a.ldq, col, a.d, q, s.live);
+        sum += store_codes<AL>(a.Q + row * a.ldq, col, a.d, q, s.live);
     }
     if (a.sums) {
         sum = row_reduce<NT>(sum, lds.sum[par], [](int x, int y) { return x + y; });
@@ -389,19 +401,19 @@ __device__ void tok_row_mem(const TokArgs& a, int64_t row, int par, TokLds<NT / 
     }
 }
 
-template <int XT, bool NORM, bool UNAL>
-__global__ __launch_bounds__(1024) void tok_mem_kernel(TokArgs a) {
-    __shared__ TokLds<1024 / WAVE> lds;
+template <int XT, int NT, bool NORM, int AL>
+__global__ __launch_bounds__(NT) void tok_mem_kernel(TokArgs a) {
+    __shared__ TokLds<NT / WAVE> lds;
     int par = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
-        if constexpr (NORM) norm_row_mem<XT, 1024, UNAL>(a, row, par, lds, false);
-        else tok_row_mem<XT, 1024, UNAL>(a, row, par, lds);
+        if constexpr (NORM) norm_row_mem<XT, NT, AL>(a, row, par, lds, false);
+        else tok_row_mem<XT, NT, AL>(a, row, par, lds);
     }
 }
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-template <int XT, int NT, int NC, int MODE, bool UNAL>
+template <int XT, int NT, int NC, int MODE, int AL>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
     constexpr int RPB = NT < 256 ? 256 / NT : 1;          // rows per workgroup (one wave each)
     constexpr bool NORM = MODE >= TOK_NORM16;
@@ -416,17 +428,19 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
         const char* xrow = (const char*)a.X + row * a.ldx * SIZE;
         Raw<XT> h[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) h[c].template load<UNAL>(xrow, col_of(c), d);
+        for (int c = 0; c < NC; ++c) h[c].template fetch<AL>(xrow, col_of(c), d);
         if constexpr (NORM) {
             if (a.R) {
                 const char* rrow = (const char*)a.R + row * a.ldr * SIZE;
                 Raw<XT> r[NC];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) r[c].template load<UNAL>(rrow, col_of(c), d);
+                for (int c = 0; c < NC; ++c) r[c].template fetch<AL>(rrow, col_of(c), d);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) h[c].add(h[c], r[c]);
             }
         }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) h[c].template settle<AL>(col_of(c), d);
         double rstd = 1.0;
         Scale s;
         double inv;
@@ -450,12 +464,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
             if constexpr (MODE == TOK_CHAN) {
                 Raw<0> cs[NC];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) cs[c].template load<UNAL>(a.chan, col_of(c), d);
+                for (int c = 0; c < NC; ++c) cs[c].template fetch<AL>(a.chan, col_of(c), d);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) cs[c].template settle<AL>(col_of(c), d);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[c][e] = !UNAL || col_of(c) + e < d ? h[c].get(e) / cs[c].get(e) : 0.f;
+                        v[c][e] = AL == ROWS_VEC || col_of(c) + e < d ? h[c].get(e) / cs[c].get(e) : 0.f;
             }
             float top = 0.f;
 #pragma unroll
@@ -475,7 +491,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
                     using G = decltype(raw);
                     G gr[NC];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) gr[c].template load<UNAL>(a.G, col_of(c), d);
+                    for (int c = 0; c < NC; ++c) gr[c].template fetch<AL>(a.G, col_of(c), d);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) gr[c].template settle<AL>(col_of(c), d);
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -517,7 +535,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
                     using G = decltype(raw);
                     G gr[NC];
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) gr[c].template load<UNAL>(a.G, col_of(c), d);
+                    for (int c = 0; c < NC; ++c) gr[c].template fetch<AL>(a.G, col_of(c), d);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) gr[c].template settle<AL>(col_of(c), d);
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -550,13 +570,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
             if (a.H) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    if (col_of(c) < d) h[c].template store<UNAL>((char*)a.H + row * a.ldh * SIZE, col_of(c), d);
+                    if (col_of(c) < d) h[c].template store<AL>((char*)a.H + row * a.ldh * SIZE, col_of(c), d);
             }
             bool finite;
             if constexpr (MODE == TOK_NORM16) {
                 m = row_reduce<NT>(m, lds.smf[par], [](SumMaxF x, SumMaxF y) { return SumMaxF{x.sum + y.sum, max_nan(x.top, y.top)}; });
                 if (!(m.top >= TOK_LOW && m.top < __builtin_inff())) {   // the same for every thread of the row
-                    norm_row_mem<XT, NT, UNAL>(a, row, par, lds, a.H != nullptr);
+                    norm_row_mem<XT, NT, AL>(a, row, par, lds, a.H != nullptr);
                     continue;
                 }
                 m64 = SumMax{m.sum, (double)m.top};
@@ -587,13 +607,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
                 // ties exact and moves nothing across them.
                 q[e] = NORM ? fma(p[e], inv, TOK_RINT) : (fma(p[e], inv, TOK_SNAP) - TOK_SNAP) + TOK_RINT;
             }
-            if (!NORM || a.Q) sum += store_codes<UNAL>(a.Q + row * a.ldq, col, d, q, s.live);
+            if (!NORM || a.Q) sum += store_codes<AL>(a.Q + row * a.ldq, col, d, q, s.live);
             if constexpr (NORM) {
                 if (a.Y) {
                     float y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] = (float)(p[e] * rstd);
-                    store_y<UNAL>(a, row, col, y);
+                    store_y<AL>(a, row, col, y);
                 }
             }
         }
@@ -604,50 +624,64 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void tok_kernel(TokArgs a) {
     }
 }
 
-template <int XT, int NT, int NC, int MODE, bool UNAL>
+template <int XT, int NT, int NC, int MODE, int AL>
 hipError_t tok_go(const TokArgs& a, hipStream_t s) {
     constexpr int RPB = NT < 256 ? 256 / NT : 1;
     const int64_t blocks = cdiv(a.T, RPB);
-    hipLaunchKernelGGL((tok_kernel<XT, NT, NC, MODE, UNAL>),
+    hipLaunchKernelGGL((tok_kernel<XT, NT, NC, MODE, AL>),
                        dim3((unsigned)(blocks < TOK_MAX_BLOCKS ? blocks : TOK_MAX_BLOCKS)), dim3(NT < 256 ? 256 : NT), 0, s, a);
     return hipGetLastError();
 }
 
-template <int XT, int MODE, bool UNAL>
+// Rows read from memory in both steps
+template <int XT, int NT, int MODE, int AL>
+hipError_t tok_go_mem(const TokArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((tok_mem_kernel<XT, NT, (MODE >= TOK_NORM16), AL>),
+                       dim3((unsigned)(a.T < TOK_MAX_BLOCKS ? a.T : TOK_MAX_BLOCKS)), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int XT, int MODE, int AL>
 hipError_t tok_pick(const TokArgs& a, hipStream_t s) {
     const int64_t d = cdiv(a.d, 8) * 8;
-    const bool few = a.T < 256;                           // fewer rows than compute units
-    if (d <= 1024 && !(few && d > 512)) return tok_go<XT, 64, 2, MODE, UNAL>(a, s);
-    if (d <= 2048) return tok_go<XT, 256, 1, MODE, UNAL>(a, s);
-    if (few && d <= 8192) return tok_go<XT, 1024, 1, MODE, UNAL>(a, s);
-    if (d <= 4096) return tok_go<XT, 256, 2, MODE, UNAL>(a, s);
-    if (d <= 8192) return tok_go<XT, 256, 4, MODE, UNAL>(a, s);
-    // longer rows: as far as they stay in registers without spills (the norm holds x, r and g at
-    // once, the float64 products the gains beside h, unaligned rows the shifted chunks)
-    if constexpr (!UNAL && MODE < TOK_NORM16) {
-        if (few && d <= 32768) return tok_go<XT, 1024, 4, MODE, UNAL>(a, s);
+    // One wave per row while it holds the row (16384 x 768 float16: 10.6 against 20.4 us with 256
+    // threads; the same at 1 row), then 256 threads (8192 x 8192 norm: 92 us, with 512 threads of
+    // 2 chunks 99, 1024 of one 160; 1 row: 4.3 / 4.2 / 4.9) with no more chunks than needed (norm of
+    // 8192 x 5120: 59 us with 3, 63 with 4), then 512 (4096 x 28672: 70 us, with 1024 of 4 chunks
+    // 75; 16 rows: 4.9 either way).
+    if (d <= 1024) return tok_go<XT, 64, 2, MODE, AL>(a, s);
+    if (d <= 2048) return tok_go<XT, 256, 1, MODE, AL>(a, s);
+    if (d <= 4096) return tok_go<XT, 256, 2, MODE, AL>(a, s);
+    if (d <= 6144) return tok_go<XT, 256, 3, MODE, AL>(a, s);
+    if (d <= 8192) return tok_go<XT, 256, 4, MODE, AL>(a, s);
+    // Longer rows: as far as they stay in registers without spills (the norm holds x, r and g at
+    // once, the float64 products the gains beside h, unaligned rows the shifted chunks), since
+    // reading a row twice takes up to twice as long (4096 x 28672: 138 against 70 us).
+    if constexpr (AL == ROWS_VEC || MODE != TOK_NORM64) {
+        if (d <= 16384) return tok_go<XT, 512, 4, MODE, AL>(a, s);
     }
-    if constexpr (!UNAL || MODE != TOK_NORM64) {
-        if (d <= 16384) return tok_go<XT, 512, 4, MODE, UNAL>(a, s);
+    if constexpr (AL == ROWS_VEC && MODE != TOK_NORM64) {
+        if (d <= 28672) return tok_go<XT, 512, 7, MODE, AL>(a, s);
     }
-    if constexpr (!UNAL && MODE != TOK_NORM64) {
-        if (d <= 28672) return tok_go<XT, 512, 7, MODE, UNAL>(a, s);
+    if constexpr (AL == ROWS_VEC && MODE < TOK_NORM16) {
+        if (d <= 32768) return tok_go<XT, 512, 8, MODE, AL>(a, s);
     }
-    if constexpr (!UNAL && MODE < TOK_NORM16) {
-        if (d <= 32768) return tok_go<XT, 512, 8, MODE, UNAL>(a, s);
-    }
-    hipLaunchKernelGGL((tok_mem_kernel<XT, (MODE >= TOK_NORM16), UNAL>),
-                       dim3((unsigned)(a.T < TOK_MAX_BLOCKS ? a.T : TOK_MAX_BLOCKS)), dim3(1024), 0, s, a);
-    return hipGetLastError();
+    return tok_go_mem<XT, 1024, MODE, AL>(a, s);
+}
+
+template <int XT, int MODE>
+hipError_t tok_rows(const TokArgs& a, bool vec, hipStream_t s) {
+    if (vec) return tok_pick<XT, MODE, ROWS_VEC>(a, s);
+    if (a.d >= 8) return tok_pick<XT, MODE, ROWS_ANY>(a, s);
+    return tok_go_mem<XT, 64, MODE, ROWS_SHORT>(a, s);
 }
 
 template <int MODE>
 hipError_t tok_type(const TokArgs& a, int x_dtype, bool vec, hipStream_t s) {
     if constexpr (MODE != TOK_NORM16) {
-        if (x_dtype == 0) return vec ? tok_pick<0, MODE, false>(a, s) : tok_pick<0, MODE, true>(a, s);
+        if (x_dtype == 0) return tok_rows<0, MODE>(a, vec, s);
     }
-    if (x_dtype == 1) return vec ? tok_pick<1, MODE, false>(a, s) : tok_pick<1, MODE, true>(a, s);
-    return vec ? tok_pick<2, MODE, false>(a, s) : tok_pick<2, MODE, true>(a, s);
+    return x_dtype == 1 ? tok_rows<1, MODE>(a, vec, s) : tok_rows<2, MODE>(a, vec, s);
 }
 
 // 16-byte loads and stores of 8 elements (8-byte ones for codes) at every multiple of 8

@@ -217,7 +217,8 @@ __device__ __forceinline__ void w8_barrier() {
 // position of chunk c in row r of a stage
 template <int BK>
 __device__ __forceinline__ int w8_pos(int r, int c) {
-    return BK == 64 ? c ^ ((4 - (r >> 2)) & 3) : (BK == 128 ? c ^ ((r >> 1) & 7) : c ^ (r & 15));
+    static_assert(BK == 64 || BK == 128, "stage");
+    return BK == 64 ? c ^ ((4 - (r >> 2)) & 3) : c ^ ((r >> 1) & 7);
 }
 
 // bid -> tile: consecutive workgroups go to different XCDs, so each XCD takes a contiguous share
