@@ -53,7 +53,7 @@ CALL_OF = [
     ("dequant_kernel", "dequant"), ("dequant_vec", "dequant"), ("dequant_f16", "dequant"),
     ("mse_", "recon_mse"), ("EpiSq", "recon_mse"), ("set_double", "recon_mse"),
     ("SplitTriMap", "recon_mse"), ("EpiTrace", "recon_mse"),
-    ("w4a16", "quantized_matmul"),
+    ("w4a16", "quantized_matmul"), ("w8_", "quantized_matmul_int8"), ("tok_", "quantize_tokens, rms_norm_quantize"),
     ("chan_abs", "channel_abs_mean"), ("chan_mean", "channel_abs_mean"),
     ("awq_", "awq_search"), ("EpiDot", "awq_search"),
     ("tensor_max", "tensor_scales"), ("tensor_scale", "tensor_scales"),
