@@ -585,6 +585,34 @@ def test_layer_of_quantized_weights(pwq, T, d, f):
     assert np.linalg.norm(f64(out) - ref) <= 0.05 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("sym", [True, False])
+@pytest.mark.parametrize("act_order", [False, True])
+def test_codes_of_a_gptq_layer(pwq, sym, act_order):
+    """A layer quantized by GPTQ to 8 bits, behind the norm: the product of what the calls wrote."""
+    rng = np.random.default_rng(5)
+    T, n, m = 9, 256, 200
+    W = torch.from_numpy((rng.standard_normal((m, n)) * 0.05).astype(np.float32)).to(DEV)
+    calib = torch.from_numpy(rng.standard_normal((1024, n)).astype(np.float32)).to(DEV)
+    x = torch.from_numpy(rng.standard_normal((T, n))).to(DEV).bfloat16()
+    q = pwq.gptq_layer(W, calib, bits=8, group_size=0, act_order=act_order, sym=sym, want_packed=False)
+    zeros = None if sym else q["zeros"]
+    a = pwq.rms_norm_quantize(x, want_sums=not sym)
+    Y = pwq.quantized_matmul_int8(a["codes"], a["scales"], q["codes"], q["scales"], zeros=zeros, x_sums=a.get("sums"),
+                                  out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want = O.quantized_matmul_int8(a["codes"].cpu().numpy(), a["scales"].cpu().numpy(), q["codes"].cpu().numpy(),
+                                   q["scales"].cpu().numpy(), zeros=None if sym else zeros.cpu().numpy())
+    assert np.all(np.abs(f64(Y) - want) <= np.abs(want) * 3.001 * 2.0 ** -24)
+    # and the layer itself: the codes' steps are the only difference from y W^T with the norm's y
+    y = O.rms_norm(f64(x), None, 1e-5)
+    sx, sw = a["scales"].cpu().numpy().astype(np.float64), f64(q["scales"]).reshape(-1)
+    cw = q["codes"].cpu().numpy().astype(np.float64) - (0 if sym else zeros.cpu().numpy().astype(np.float64).reshape(-1, 1))
+    exact = y @ (cw * sw[:, None]).T
+    # each activation is off by at most half a step of its token (and the scale's rounding)
+    bound = sx[:, None] * 0.5001 * np.sum(np.abs(cw * sw[:, None]), axis=1)[None, :]
+    assert np.all(np.abs(f64(Y) - exact) <= bound + np.abs(want) * 2.0 ** -20)
+
+
 @pytest.mark.parametrize("T,d,f", [(1, 2048, 4096), (40, 770, 512)])
 def test_layer_captured_and_replayed(pwq, T, d, f):
     """The path in a HIP graph, replayed on new inputs with eager work between the replays, and on
