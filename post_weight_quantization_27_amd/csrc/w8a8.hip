@@ -194,13 +194,15 @@ __device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, i
 //           least LDS traffic of the copies, for large tiles.
 //   KG = 2: each group takes every other stage of k for the whole tile (WO x 4 / WO waves), with
 //           stages of its own that its own waves copy; the two sums meet in LDS at the end.
-//           The wave tiles are twice as large, which saves a third of the LDS reads on tiles
-//           that eight waves would cut too small.
+//           The wave tiles are twice as large, which saves a third of the LDS reads on 64 x 64
+//           tiles (48 tokens by 14336 x 4096: 14.3 against 15.3 us; 128 x 64 tiles are better off
+//           with KG = 1 and a fourth stage: 64 tokens by 28672 x 8192 42 against 46 us, 2048 by
+//           768 x 768 6.1 against 6.8, though 2048 by 1008 x 4096 16.0 against 14.5).
 //
 // Measured: 8192^3 440-460 us, 8192 tokens by 28672 x 8192 1550-1620 us (2.4-2.5 POP/s; bound by
 // power: the clock falls to 1.75 GHz, at which the matrix units are busy 78 % of the time); 512
 // tokens by 8192 x 8192 36 us (128 x 128 tiles, one per compute unit: 130 KB through LDS per 128 k
-// are 1024 cycles at 128 bytes each, twice the multiplies'); 48 tokens by 28672 x 8192 47 us (5.1
+// are 1024 cycles at 128 bytes each, twice the multiplies'); 48 tokens by 28672 x 8192 43 us (5.6
 // TB/s of codes); one token by 8192 x 28672 41 us and 4.7 for the join (5.7 TB/s without it).
 // Stages of 64 k at KG = 2, which would fit 128 x 128 and 128 x 256 tiles, move 64-byte pieces of
 // rows and take 30 % longer.
@@ -765,10 +767,10 @@ constexpr int W8_TILES = sizeof(w8_tiles) / sizeof(w8_tiles[0]);
 // The least estimate (us) of: rounds of tiles on 256 compute units, each a fixed part and its steps
 // of k, over 1 to 8 splits of k whose sums a second launch joins, and no less than memory takes;
 // or the row kernel, whose workgroups stream their 16 rows of codes once per 16 tokens, at 19.5
-// bytes per ns each.  The constants are fitted to the times of every kernel over 544 shapes (512 ..
-// 32000 inputs and outputs, 1 .. 4096 tokens): the choice takes 0.7 % longer than the fastest
-// kernel in the geometric mean and 22 % at the worst (256 tokens by 4096 x 1008: 11.3 against
-// 9.2 us); 128 x 128 tiles alone take 60 % longer in the mean and up to 3.5 times as long.
+// bytes per ns each.  The constants are fitted to the times of every kernel over some 600 shapes
+// (512 .. 32000 inputs and outputs, 1 .. 4096 tokens): the choice takes 0.7 % longer than the
+// fastest kernel in the geometric mean and 30 % at the worst (150 tokens by 4096 x 11008: 29.9
+// against 23.0 us); 128 x 128 tiles alone take 58 % longer in the mean and up to 3.6 times as long.
 W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
     const double bytes = ((double)T * n + (double)m * n + 2.0 * T * m) * 1e-6;          // MB
     const double mem = bytes / 6.8 + 4.9;
@@ -836,7 +838,7 @@ hipError_t w8_run(W8Args a, const W8Plan& p, hipStream_t s) {
         case 0: e = w8_tile_go<256, 256, 64, 5, 4, 1>(a, s); break;
         case 1: e = w8_tile_go<128, 256, 128, 3, 2, 1>(a, s); break;
         case 2: e = w8_tile_go<128, 128, 128, 4, 2, 1>(a, s); break;
-        case 3: e = w8_tile_go<128, 64, 128, 3, 2, 2>(a, s); break;
+        case 3: e = w8_tile_go<128, 64, 128, 4, 4, 1>(a, s); break;
         case 4: e = w8_tile_go<64, 64, 128, 4, 2, 2>(a, s); break;
         case W8_ROW2: e = w8_row_go<2>(a, s); break;
         case W8_ROW4: e = w8_row_go<4>(a, s); break;
