@@ -27,8 +27,8 @@
 // run beside another's stores.  Rows too long for the registers are read again for the second
 // step.  Measured: norm of 8192 x 8192 bf16 with a residual 92-97 us (4.8-5.1 TB/s, as a copy of
 // as many bytes), rows that start at any byte 122 us; token quantizer of 4096 x 28672 bf16
-// 70-79 us (4.5-5.1 TB/s), with a channel scale 119 us (its division and its loads, which are
-// twice X's); one row of 8192 4.3 us, an empty launch 2.2.
+// 70-80 us (4.4-5.0 TB/s), with a channel scale 119 us (its loads, twice X's bytes from L2 for
+// every row, take 35 more and its exact division 17); one row of 8192 4.3 us, an empty launch 2.2.
 #pragma once
 
 #include "../../include/pwq.h"
