@@ -480,7 +480,7 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 }
 
 // ------------------------------------------------------------------ any alignment
-// GT x GT tile, four waves as 2 x 2, 128 k per step: rows may start at any byte and have any
+// BO x BT tile (outputs x tokens), four waves as 2 x 2, 128 k per step: rows may start at any byte and have any
 // length.  Operands travel through registers into the same LDS layout as the tiles above, P steps
 // ahead of their use; LDS has two buffers and a step one barrier.  No load stands behind a branch,
 // so that the wait for one step's loads leaves the later steps' in flight.
@@ -489,10 +489,11 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 // down in registers, with 0 behind (X's zeros make the codes' bytes there irrelevant), fetched
 // ahead like the others.
 //
-// 333 tokens by 5003 outputs: 10 us with rows of 1664 (whole cache lines; the tiles above), 13.4
-// with 1604 (a chunk of 128 takes two lines), 15.3 with 1602 and 17.3 with 1601 (16 bytes from an
-// odd address take the load path about twice as long; loads of the words around them, moved down
-// by 0 to 3 bytes, are 1 to 5 % faster there and 10 % slower at few tokens, as they are five).
+// 333 tokens by 5003 outputs: 10 us with rows of 1664 (whole cache lines; the tiles above), 12.0
+// with 1604 (a chunk of 128 takes two lines) and 13.7 with 1601 (16 bytes from an odd address take
+// the load path about twice as long, so tiles that read an operand less often gain).  Loads of the
+// words around them, moved down by 0 to 3 bytes, were 1 to 5 % faster there and 10 % slower at
+// few tokens, as they are five.
 
 // The 16 bytes from byte `by` (0 .. 16) on, with 0 behind them
 __device__ __forceinline__ uint4 w8_drop(uint4 v, int by) {
@@ -516,28 +517,29 @@ __device__ __forceinline__ uint4 w8_short(const uint8_t* row, int64_t k, int64_t
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int GT, int P, bool ZP>
+template <int BO, int BT, int P, bool ZP>
 __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
-    constexpr int BK = 128, F = GT / 32, NC = GT * 2 * 8 / 256;       // fragments per wave side, chunks per thread
-    constexpr int ST = 2 * GT * BK;
+    constexpr int BK = 128, FO = BO / 32, FT = BT / 32;       // fragments of a wave
+    constexpr int NC = (BO + BT) / 32;                        // chunks per thread
+    constexpr int ST = (BO + BT) * BK;
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * ST];
     int to, tt;
     w8_map(a, blockIdx.x, to, tt);
-    const int64_t o0 = (int64_t)to * GT, t0 = (int64_t)tt * GT;
+    const int64_t o0 = (int64_t)to * BO, t0 = (int64_t)tt * BT;
     const int64_t kbeg = (int64_t)blockIdx.y * a.kper;
     const int64_t kend = kbeg + a.kper < a.n ? kbeg + a.kper : a.n;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wo = wave & 1, wt = wave >> 1;
 
-    // chunk j of this thread: chunk tid % 8 of row j 32 + tid / 8 of the codes' GT rows followed by
-    // the activations' GT; rows past the matrices repeat the last one (not stored)
+    // chunk j of this thread: chunk tid % 8 of row j 32 + tid / 8 of the codes' BO rows followed by
+    // the activations' BT; rows past the matrices repeat the last one (not stored)
     const uint8_t* src[NC];
     int dst[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
         const int r = j * 32 + (tid >> 3);
-        if (r < GT) src[j] = a.C + (o0 + r < a.m ? o0 + r : a.m - 1) * a.n;
-        else src[j] = (const uint8_t*)a.X + (t0 + r - GT < a.T ? t0 + r - GT : a.T - 1) * a.ldx;
+        if (r < BO) src[j] = a.C + (o0 + r < a.m ? o0 + r : a.m - 1) * a.n;
+        else src[j] = (const uint8_t*)a.X + (t0 + r - BO < a.T ? t0 + r - BO : a.T - 1) * a.ldx;
         dst[j] = r * BK + 16 * w8_pos<BK>(r & 15, tid & 7);
     }
     const int nsteps = (int)cdiv(kend - kbeg, BK), nfull = (int)((kend - kbeg) / BK);
@@ -550,11 +552,11 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
 #pragma unroll
         for (int j = 0; j < NC; ++j) __builtin_memcpy(&v[j], src[j] + k, 16);
     };
-    i32x4 acc[F][F];
+    i32x4 acc[FO][FT];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FO; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+        for (int j = 0; j < FT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
     const int r = lane & 15, c = lane >> 4;
     auto multiply = [&](const uint8_t* S) {
         w8_wait_lds();
@@ -562,21 +564,20 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
 #pragma unroll
         for (int ks = 0; ks < BK / 64; ++ks) {
             const int o = r * BK + 16 * w8_pos<BK>(r, 4 * ks + c);
-            i32x4 fo[F], ft[F];
+            i32x4 fo[FO], ft[FT];
 #pragma unroll
-            for (int i = 0; i < F; ++i) {
-                fo[i] = *(const i32x4*)(S + (wo * (GT / 2) + 16 * i) * BK + o);
-                ft[i] = *(const i32x4*)(S + (GT + wt * (GT / 2) + 16 * i) * BK + o);
-            }
+            for (int i = 0; i < FO; ++i) fo[i] = *(const i32x4*)(S + (wo * (BO / 2) + 16 * i) * BK + o);
 #pragma unroll
-            for (int i = 0; i < F; ++i)
+            for (int j = 0; j < FT; ++j) ft[j] = *(const i32x4*)(S + (BO + wt * (BT / 2) + 16 * j) * BK + o);
 #pragma unroll
-                for (int j = 0; j < F; ++j)
+            for (int i = 0; i < FO; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fo[i], ft[j], acc[i][j], 0, 0, 0);
         }
     };
     auto put = [&](uint8_t* S, int j, uint4 w) {
-        if (ZP && j < NC / 2) { w.x ^= 0x80808080u; w.y ^= 0x80808080u; w.z ^= 0x80808080u; w.w ^= 0x80808080u; }
+        if (ZP && j < BO / 32) { w.x ^= 0x80808080u; w.y ^= 0x80808080u; w.z ^= 0x80808080u; w.w ^= 0x80808080u; }
         *(uint4*)(S + dst[j]) = w;
     };
     // step `it` (a whole one: 128 k), whose chunks are in v; v is refilled for a later one under its
@@ -612,17 +613,17 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
         for (int j = 0; j < NC; ++j) put(lds, j, w8_short(src[j], 16 * (tid & 7), a.n));
         multiply(lds);
     }
-    W8Quad q[F];
-    W8Tok tok[F];
-    const int64_t ob = o0 + wo * (GT / 2) + 4 * c, tb = t0 + wt * (GT / 2) + r;
+    W8Quad q[FO];
+    W8Tok tok[FT];
+    const int64_t ob = o0 + wo * (BO / 2) + 4 * c, tb = t0 + wt * (BT / 2) + r;
 #pragma unroll
-    for (int i = 0; i < F; ++i) q[i] = w8_quad(a, ob + 16 * i);
+    for (int i = 0; i < FO; ++i) q[i] = w8_quad(a, ob + 16 * i);
 #pragma unroll
-    for (int j = 0; j < F; ++j) tok[j] = w8_tok(a, tb + 16 * j);
+    for (int j = 0; j < FT; ++j) tok[j] = w8_tok(a, tb + 16 * j);
 #pragma unroll
-    for (int j = 0; j < F; ++j)
+    for (int j = 0; j < FT; ++j)
 #pragma unroll
-        for (int i = 0; i < F; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
+        for (int i = 0; i < FO; ++i) w8_out4<ZP>(a, acc[i][j], tb + 16 * j, ob + 16 * i, q[i], tok[j]);
 }
 
 // ------------------------------------------------------------------ few tokens
@@ -730,7 +731,7 @@ struct W8Plan {
     int splits;
     int64_t kper;
 };
-constexpr int W8_ANY64 = -1, W8_ANY128 = -2, W8_ROW2 = -3, W8_ROW4 = -4;
+constexpr int W8_ROW2 = -1, W8_ROW4 = -2, W8_ANY = 8;     // and W8_ANY + an index into w8_any
 
 // k over `s` splits in whole steps of `step`
 W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
@@ -738,15 +739,40 @@ W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
     return W8Plan{kind, (int)cdiv(n, kper), kper};
 }
 
-// Any alignment: tiles of 64 x 64 while there are few (a split of k would pay another launch), of
-// 128 x 128 from 1024 of those on.
+// Any alignment: the tile and the splits of k with the least estimate (us), rounds of tiles as below,
+// of which workgroups that share a compute unit overlap a part.  Fitted to the times over 289 shapes
+// (100 .. 28670 inputs, most of them odd, 500 .. 28671 outputs, 1 .. 2000 tokens): 0.7 % longer
+// than the fastest in the geometric mean and 19 % at the worst; 64 x 64 tiles alone, 128 x 128 from
+// 1024 of those on, take 20 % longer in the mean.  333 tokens by 5003 x 1601: 13.7 us with 64 x 128,
+// 16.4 with 64 x 64; 16 tokens by 28671 x 8191: 58 with 128 x 32, 67 with 128 x 64; 1 token by 4099
+// x 4095: 11.6 with 64 x 32 in two splits, 15 with 64 x 64 in one.
+struct W8AnyCost {
+    int bo, bt;
+    float fixed, step;             // us per tile, and for each 128 k
+};
+constexpr W8AnyCost w8_any[] = {
+    {64, 32, 0.55f, 0.29f}, {128, 32, 1.1f, 0.56f}, {64, 64, 1.1f, 0.42f}, {64, 128, 1.25f, 0.61f}, {128, 128, 2.7f, 1.05f},
+};
 W8Plan w8_plan_any(int64_t T, int64_t n, int64_t m) {
-    const int64_t big = cdiv(T, 128) * cdiv(m, 128);
-    if (big >= 1024) return w8_split(W8_ANY128, n, 1, 128);
-    const int64_t tiles = cdiv(T, 64) * cdiv(m, 64);
-    int64_t s = 256 / tiles;
-    if (s > n / 2048) s = n / 2048;
-    return w8_split(W8_ANY64, n, s, 128);
+    const double mem = ((double)T * n + (double)m * n + 2.0 * T * m) * 1e-6 / 5.0 + 4.0;
+    W8Plan best{W8_ANY, 1, n};
+    double least = 1e30;
+    for (int i = 0; i < (int)(sizeof(w8_any) / sizeof(w8_any[0])); ++i) {
+        const W8AnyCost& c = w8_any[i];
+        const int64_t tiles = cdiv(T, c.bt) * cdiv(m, c.bo);
+        for (int64_t s = 1; s <= 8; s *= 2) {
+            if (s > 1 && n / s < W8_SPLIT_MIN_K) break;
+            const W8Plan p = w8_split(W8_ANY + i, n, s, 128);
+            if (s > 1 && p.splits < s) continue;
+            const double groups = (double)(tiles * p.splits) / 256.0, rounds = (double)cdiv(tiles * p.splits, 256);
+            const double load = 0.25 * (groups > 1.0 ? groups : 1.0) + 0.75 * rounds;
+            double t = 3.3 + c.fixed * rounds + c.step * (double)cdiv(p.kper, 128) * load;
+            t = (t > mem ? t : mem) + 0.001 * t;
+            if (p.splits > 1) t += 2.6 + 0.5 * (double)p.splits * T * m * 4e-6;
+            if (t < least) { least = t; best = p; }
+        }
+    }
+    return best;
 }
 
 // The tiles, and what one costs on this chip: every compute unit holds one workgroup, which takes
@@ -820,13 +846,13 @@ hipError_t w8_row_go(const W8Args& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int GT, int P>
+template <int BO, int BT, int P>
 hipError_t w8_any_go(W8Args a, hipStream_t s) {
-    a.tiles_m = (int)cdiv(a.m, GT);
-    a.tiles_t = (int)cdiv(a.T, GT);
+    a.tiles_m = (int)cdiv(a.m, BO);
+    a.tiles_t = (int)cdiv(a.T, BT);
     const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
-    if (a.zeros) hipLaunchKernelGGL((w8_any_kernel<GT, P, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((w8_any_kernel<GT, P, false>), grid, dim3(256), 0, s, a);
+    if (a.zeros) hipLaunchKernelGGL((w8_any_kernel<BO, BT, P, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((w8_any_kernel<BO, BT, P, false>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -842,8 +868,11 @@ hipError_t w8_run(W8Args a, const W8Plan& p, hipStream_t s) {
         case 4: e = w8_tile_go<64, 64, 128, 4, 2, 2>(a, s); break;
         case W8_ROW2: e = w8_row_go<2>(a, s); break;
         case W8_ROW4: e = w8_row_go<4>(a, s); break;
-        case W8_ANY64: e = w8_any_go<64, 4>(a, s); break;
-        default: e = w8_any_go<128, 2>(a, s); break;
+        case W8_ANY: e = w8_any_go<64, 32, 4>(a, s); break;
+        case W8_ANY + 1: e = w8_any_go<128, 32, 4>(a, s); break;
+        case W8_ANY + 2: e = w8_any_go<64, 64, 4>(a, s); break;
+        case W8_ANY + 3: e = w8_any_go<64, 128, 3>(a, s); break;
+        default: e = w8_any_go<128, 128, 2>(a, s); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const dim3 grid((unsigned)cdiv(a.m, 1024), (unsigned)(a.T < 32768 ? a.T : 32768));
@@ -855,7 +884,8 @@ hipError_t w8_run(W8Args a, const W8Plan& p, hipStream_t s) {
 }  // namespace
 
 bool w8_size_ok(int64_t T, int64_t m) {
-    // work-items of a launch are counted in 32 bits: workgroups of 512 for tiles of 64 x 64 at least
+    // work-items of a launch are counted in 32 bits: workgroups of 512 for tiles of 64 x 64 at least, of
+    // 256 for 64 x 32
     return cdiv(T, 64) * cdiv(m, 64) < ((int64_t)1 << 23) && cdiv(m, 16) < ((int64_t)1 << 23);
 }
 

@@ -424,6 +424,14 @@ def test_quantized_matmul_int8_several_tiles_per_workgroup(pwq, T, n, m, zp, odt
     test_quantized_matmul_int8_large_sampled(pwq, T, n, m, zp, odt)
 
 
+@pytest.mark.parametrize("T,n,m,zp,odt", [(333, 1601, 5003, True, "f32"), (16, 8191, 28671, False, "bf16"), (2, 4095, 4099, True, "f16"),
+                                          (48, 8190, 4099, False, "f16"), (2000, 5001, 5000, True, "bf16"), (1300, 301, 2002, False, "f32"),
+                                          (40, 3001, 9001, True, "f32"), (130, 1023, 28670, True, "bf16"), (65, 65535, 70, True, "f32")])
+def test_quantized_matmul_int8_any_alignment(pwq, T, n, m, zp, odt):
+    """Rows that start at any byte: sizes that take each tile, with and without splits of k."""
+    test_quantized_matmul_int8_large_sampled(pwq, T, n, m, zp, odt)
+
+
 def test_quantized_matmul_int8_scales(pwq):
     """Scales at the ends of their ranges: a token of scale 0 or NaN, products that a scale alone
     would carry out of float32's range."""
