@@ -481,7 +481,8 @@ pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int6
  *             aligned (0 bytes: ws may be NULL): the int32 sums of a split k.
  * Any alignment and sizes with 1 <= d_in <= 65535; rows of X and codes that start at multiples
  * of 16 bytes (16-byte aligned pointers, ldx and d_in multiples of 16) take the faster kernels.
- * PWQ_EINVAL when Y needs more tiles of 64 x 64 than one launch holds (2^23). */
+ * PWQ_EINVAL when Y needs more tiles of 64 x 64 than one launch holds (2^23), or d_out is 2^27
+ * or more.  Calls that may run at the same time need a ws each. */
 size_t pwq_quantized_matmul_int8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out);
 pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const float* x_scales,
                                      const int32_t* x_sums, const void* codes, const uint16_t* scales,

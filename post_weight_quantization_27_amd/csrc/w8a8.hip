@@ -480,10 +480,10 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 }
 
 // ------------------------------------------------------------------ any alignment
-// BO x BT tile (outputs x tokens), four waves as 2 x 2, 128 k per step: rows may start at any byte and have any
-// length.  Operands travel through registers into the same LDS layout as the tiles above, P steps
-// ahead of their use; LDS has two buffers and a step one barrier.  No load stands behind a branch,
-// so that the wait for one step's loads leaves the later steps' in flight.
+// BO x BT tile (outputs x tokens), four waves as 2 x 2, 128 k per step: rows may start at any byte
+// and have any length.  Operands travel through registers into the same LDS layout as the tiles
+// above, P steps ahead of their use; LDS has two buffers and a step one barrier.  No load stands
+// behind a branch, so that the wait for one step's loads leaves the later steps' in flight.
 //
 // The last step may be partial: each 16 bytes past the end is the row's last 16 instead, moved
 // down in registers, with 0 behind (X's zeros make the codes' bytes there irrelevant), fetched
