@@ -442,7 +442,9 @@ pwq_status pwq_quantized_matmul_noalloc(const void* X, int x_dtype, int64_t n_to
  *   channel_scale  optional float32[d].
  *   codes          int8 n_tok x d, leading dimension ldq; scales float32[n_tok].
  *   sums           optional int32[n_tok].
- * Codes are those of the exact quotient y / s.  1 <= d <= 65535. */
+ * Codes are those of the exact quotient y / s.  1 <= d <= 65535.  In this call and the two below,
+ * PWQ_EINVAL where an output shares a byte with an input or with another output (columns of one
+ * wider matrix, whose rows lie between each other's, share none). */
 pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx,
                                const float* channel_scale, int8_t* codes, int64_t ldq, float* scales, int32_t* sums,
                                void* stream);
@@ -455,8 +457,7 @@ pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_
  *   gain      optional d values of gain_dtype (any of the three types; NULL: ones).
  *   eps       >= 0 (a row of zeros with eps 0 is not finite).
  *   h_out     optional n_tok x d of x_dtype, leading dimension ldh; may be X or residual
- *             themselves (same pointer and stride), no other outputs may overlap inputs.
- *             Needs residual.
+ *             themselves (same pointer and stride).  Needs residual.
  *   codes, scales, sums  as above; codes and scales together, or both NULL (then sums too).
  *   Y         optional: y itself, rounded to y_dtype, leading dimension ldy (the input of
  *             pwq_quantized_matmul as float16).  At least one of codes / Y.

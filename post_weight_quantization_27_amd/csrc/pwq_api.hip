@@ -8,6 +8,7 @@
 
 #include "../../include/pwq.h"
 #include "pwq_internal.h"
+#include "overlap.h"
 
 using namespace pwq;
 
@@ -502,6 +503,9 @@ pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_
     if (!X || !codes || !scales || !aligned(X, float_size(x_dtype)) || !aligned(channel_scale, 4) || !aligned(scales, 4) ||
         !aligned(sums, 4))
         return PWQ_EINVAL;
+    const Rows out[] = {rows_of(codes, n_tok, d, ldq, 1), bytes_of(scales, 4 * n_tok), bytes_of(sums, 4 * n_tok)};
+    const Rows in[] = {rows_of(X, n_tok, d, ldx, float_size(x_dtype)), bytes_of(channel_scale, 4 * d)};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
     return hip_status(tok_quant_launch(X, x_dtype, n_tok, d, ldx, channel_scale, codes, ldq, scales, sums,
                                        (hipStream_t)stream));
 }
@@ -522,6 +526,15 @@ pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int6
     if (!aligned(X, e) || !aligned(residual, e) || !aligned(h_out, e) || (gain && !aligned(gain, float_size(gain_dtype))) ||
         !aligned(scales, 4) || !aligned(sums, 4) || (Y && !aligned(Y, float_size(y_dtype))))
         return PWQ_EINVAL;
+    const Rows x = rows_of(X, n_tok, d, ldx, e), r = rows_of(residual, n_tok, d, ldr, e), h = rows_of(h_out, n_tok, d, ldh, e);
+    const Rows g = bytes_of(gain, gain ? d * float_size(gain_dtype) : 0);
+    const Rows out[] = {rows_of(codes, n_tok, d, ldq, 1), bytes_of(scales, 4 * n_tok), bytes_of(sums, 4 * n_tok),
+                        rows_of(Y, n_tok, d, ldy, Y ? float_size(y_dtype) : 0), h};
+    // h may be x or the residual itself: each row is read by those who write it, before they do
+    const Rows none{0, 0, 0, 0};
+    auto same = [&](const Rows& a) { return a.p == h.p && (a.pitch == h.pitch || n_tok == 1); };
+    const Rows in[] = {same(x) ? none : x, same(r) ? none : r, g};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
     return hip_status(rms_norm_launch(X, x_dtype, n_tok, d, ldx, residual, ldr, gain, gain_dtype, eps, h_out, ldh, codes,
                                       ldq, scales, sums, Y, y_dtype, ldy, (hipStream_t)stream));
 }
@@ -549,6 +562,10 @@ pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_i
         return PWQ_EINVAL;
     const size_t need = pwq_quantized_matmul_int8_workspace_size(n_tok, d_in, d_out);
     if (need && (!ws || ws_bytes < need || !aligned(ws, 16))) return PWQ_EWORKSPACE;
+    const Rows out[] = {rows_of(Y, n_tok, d_out, ldy, float_size(y_dtype)), bytes_of(need ? ws : nullptr, (int64_t)need)};
+    const Rows in[] = {rows_of(X, n_tok, d_in, ldx, 1), bytes_of(codes, d_out * d_in), bytes_of(x_scales, 4 * n_tok),
+                       bytes_of(zeros ? x_sums : nullptr, 4 * n_tok), bytes_of(scales, 2 * d_out), bytes_of(zeros, 2 * d_out)};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
     return hip_status(w8_launch(X, n_tok, d_in, ldx, x_scales, zeros ? x_sums : nullptr, (const uint8_t*)codes, scales,
                                 zeros, d_out, Y, y_dtype, ldy, ws, (hipStream_t)stream));
 }

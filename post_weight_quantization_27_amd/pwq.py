@@ -558,7 +558,8 @@ def rms_norm_quantize(X: torch.Tensor, gain: Optional[torch.Tensor] = None, resi
     want_sums)} as quantize_tokens gives them for y, h (the sum, in X's type, with a residual;
     ``out={"h": residual}`` updates it in place), y (with ``y_dtype``: y rounded to that type,
     e.g. the float16 input of quantized_matmul; ``want_codes=False`` for y alone).  Every tensor of
-    ``out`` with one of these names is written; none but h may share memory with an input."""
+    ``out`` with one of these names is written; one that shares memory with an input is refused,
+    but for h as X or the residual itself."""
     dev = X.device
     if dev.type != "cuda":
         _bad("X", "a GPU tensor")
