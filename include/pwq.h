@@ -433,8 +433,9 @@ pwq_status pwq_quantized_matmul_noalloc(const void* X, int x_dtype, int64_t n_to
  *   s    = float32(max |y| / 127); below 2^-120 it counts as 0
  *   code = nearest integer to y / s, ties to even, so -127 .. 127; s = 0 gives code 0
  * A token with a value that is not finite gets scale NaN and codes 0, so that its products
- * come out NaN.  sums[t] = sum of the token's codes, what pwq_quantized_matmul_int8 needs for
- * the zero-point form.
+ * come out NaN (one whose finite values pass 127 times float32's largest: scale infinity, codes
+ * 0, products NaN too).  sums[t] = sum of the token's codes, what pwq_quantized_matmul_int8 needs
+ * for the zero-point form.
  *
  * pwq_quantize_tokens: y = X, or with channel_scale the float32 quotient X[t][c] /
  * channel_scale[c] (s_out of pwq_awq_search: "at inference X is divided by s_out").
@@ -461,7 +462,12 @@ pwq_status pwq_quantize_tokens(const void* X, int x_dtype, int64_t n_tok, int64_
  *   codes, scales, sums  as above; codes and scales together, or both NULL (then sums too).
  *   Y         optional: y itself, rounded to y_dtype, leading dimension ldy (the input of
  *             pwq_quantized_matmul as float16).  At least one of codes / Y.
- * 1 <= d <= 65535.  Each value is read and written once; nothing is allocated. */
+ * 1 <= d <= 65535; nothing is allocated.  A value is written once, and read once while a workgroup's
+ * registers hold its row: d up to 28672 with float16 or bfloat16 X and gains of these types (or
+ * none), 16384 with float32 X or gains, where d and all strides are multiples of 8 and the
+ * pointers 16-byte aligned (codes 8-byte); 16384 and 8192 otherwise.  Longer rows, rows of less
+ * than 8, and 16-bit rows whose products h * gain are very small (all zero too) or not finite in
+ * float32 are read twice.  y reaches a 16-bit y_dtype through float32 (two roundings). */
 pwq_status pwq_rms_norm_quantize(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx, const void* residual,
                                  int64_t ldr, const void* gain, int gain_dtype, double eps, void* h_out, int64_t ldh,
                                  int8_t* codes, int64_t ldq, float* scales, int32_t* sums, void* Y, int y_dtype,

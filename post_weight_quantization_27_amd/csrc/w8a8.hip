@@ -199,11 +199,16 @@ __device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, i
 //           with KG = 1 and a fourth stage: 64 tokens by 28672 x 8192 42 against 46 us, 2048 by
 //           768 x 768 6.1 against 6.8, though 2048 by 1008 x 4096 16.0 against 14.5).
 //
-// Measured: 8192^3 440-460 us, 8192 tokens by 28672 x 8192 1550-1620 us (2.4-2.5 POP/s; bound by
-// power: the clock falls to 1.75 GHz, at which the matrix units are busy 78 % of the time); 512
-// tokens by 8192 x 8192 36 us (128 x 128 tiles, one per compute unit: 130 KB through LDS per 128 k
-// are 1024 cycles at 128 bytes each, twice the multiplies'); 48 tokens by 28672 x 8192 43 us (5.6
-// TB/s of codes); one token by 8192 x 28672 41 us and 4.7 for the join (5.7 TB/s without it).
+// Measured (kernel trace, operands cold): 8192^3 440-445 us, 8192 tokens by 28672 x 8192 1540-1640 us
+// (2.3-2.5 POP/s).  The clock falls to 1.83 and 1.63 GHz there, which is what power leaves of 2.4, and
+// the matrix units are busy 64 and 69 % of its cycles.  512 tokens by 8192 x 8192 41 us, 36 with the
+// operands in the last cache (128 x 128 tiles, one per compute unit: 130 KB through LDS per 128 k
+// are 1024 cycles at 128 bytes each, twice the multiplies', and the matrix units are busy 41 % of
+// the time); 48 tokens by 28672 x 8192 43-45 us (5.3-5.6 TB/s of codes); one token by 8192 x 28672
+// 41-43 us and 4.6 for the join (5.4-5.7 TB/s without it).  Between 17 and 512 tokens the tiles are
+// far from both bounds: 64 by 8192 x 8192 26 us (the codes alone 11), 192 by 28672 x 8192 71 (41), 256
+// by 17920 x 5120 47 (21), 320 by 28672 x 8192 102 (68): tiles padded with tokens that are not
+// there, and too few of them for the chip.
 // Stages of 64 k at KG = 2, which would fit 128 x 128 and 128 x 256 tiles, move 64-byte pieces of
 // rows and take 30 % longer.
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -246,7 +251,8 @@ __device__ __forceinline__ void w8_map(const W8Args& a, int bid, int& to, int& t
 
 // One workgroup per compute unit that goes through its tiles (3-4 % over a workgroup per tile on
 // 8192 x 8192 x 2048 and 8192^3), where the registers allow it: with 256 x 256 tiles it gains
-// nothing and the zero-point form spills.
+// nothing and the zero-point form spills.  (These keep the next tile's addresses beside this one's
+// and spill 52 to 63 scalar registers into lanes of vector registers, none to memory.)
 template <int BO, int BT, int KG>
 constexpr bool w8_persist = KG == 1 && BO * BT < 65536;
 
@@ -489,11 +495,15 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 // down in registers, with 0 behind (X's zeros make the codes' bytes there irrelevant), fetched
 // ahead like the others.
 //
-// 333 tokens by 5003 outputs: 10 us with rows of 1664 (whole cache lines; the tiles above), 12.0
-// with 1604 (a chunk of 128 takes two lines) and 13.7 with 1601 (16 bytes from an odd address take
-// the load path about twice as long, so tiles that read an operand less often gain).  Loads of the
-// words around them, moved down by 0 to 3 bytes, were 1 to 5 % faster there and 10 % slower at
-// few tokens, as they are five.
+// 333 tokens by 5003 outputs in 16 bits, in a loop over cold codes: 9.8 us with rows of 1664 (whole
+// cache lines; the tiles above), 12 with 1604 (a chunk of 128 takes two lines) and 14 with 1601 (16
+// bytes from an odd address take the load path about twice as long, so tiles that read an operand
+// less often gain); there with zero-points and float32 outputs 16.  Loads of the words around
+// them, moved down by 0 to 3 bytes, were 1 to 5 % faster there and 10 % slower at few tokens, as
+// they are five.  Long prompts are 2 to 3 times as long as on aligned rows (2000 tokens by 28671 x
+// 8191: 1040 us; 2048 by 28672 x 8192: 444), more than copying both operands to aligned rows
+// would cost; with 128 x 128 tiles the symmetric form needs 258 registers, two too many for a
+// second workgroup on a compute unit, the zero-point form 248.
 
 // The 16 bytes from byte `by` (0 .. 16) on, with 0 behind them
 __device__ __forceinline__ uint4 w8_drop(uint4 v, int by) {
@@ -632,8 +642,8 @@ __global__ __launch_bounds__(256) void w8_any_kernel(W8Args a) {
 // 64 U, every lane loads its fragments (16 bytes of one row) straight into registers, those of a
 // turn while the turn before is multiplied, and the waves' sums meet in LDS.  No staging: a code
 // is used once, and X comes from L2.  Loads past the rows or tokens take a 16-byte block of
-// zeros as their address, so none waits behind a branch.  Measured: one token by 768 x 768
-// 3.1 us, by 8192 x 8192 14.8 us (4.5 TB/s; an empty launch takes 2.2).
+// zeros as their address, so none waits behind a branch.  Measured (kernel trace, codes cold): one
+// token by 768 x 768 3.4 us, by 8192 x 8192 16 us (4.2 TB/s; an empty launch takes 2.2).
 template <int U, bool ZP>
 __global__ __launch_bounds__(512) void w8_row_kernel(W8Args a) {
     __shared__ i32x4 red[8][64];
@@ -697,7 +707,7 @@ __global__ __launch_bounds__(512) void w8_row_kernel(W8Args a) {
 }
 
 // ------------------------------------------------------------------ splits
-// The splits' sums of four outputs of a token at a time, scaled (one token, 8192 outputs: 4.7 us, a
+// The splits' sums of four outputs of a token at a time, scaled (one token, 8192 outputs: 4.6 us, a
 // launch and two round trips to memory).  grid: x = outputs, y = tokens
 template <bool ZP>
 __global__ __launch_bounds__(256) void w8_join_kernel(W8Args a) {

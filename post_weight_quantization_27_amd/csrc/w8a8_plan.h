@@ -28,9 +28,10 @@ inline W8Plan w8_split(int kind, int64_t n, int64_t s, int64_t step) {
 // of which workgroups that share a compute unit overlap a part.  Fitted to the times over 289 shapes
 // (100 .. 28670 inputs, most of them odd, 500 .. 28671 outputs, 1 .. 2000 tokens): 0.7 % longer
 // than the fastest in the geometric mean and 19 % at the worst; 64 x 64 tiles alone, 128 x 128 from
-// 1024 of those on, take 20 % longer in the mean.  333 tokens by 5003 x 1601: 13.7 us with 64 x 128,
-// 16.4 with 64 x 64; 16 tokens by 28671 x 8191: 58 with 128 x 32, 67 with 128 x 64; 1 token by 4099
-// x 4095: 11.6 with 64 x 32 in two splits, 15 with 64 x 64 in one.
+// 1024 of those on, take 20 % longer in the mean.  In a loop over cold codes, float16 outputs: 333
+// tokens by 5003 x 1601 13.7 us with 64 x 128, 16.6 with 64 x 64; 16 tokens by 28671 x 8191 58 with
+// 128 x 32, 66 with 64 x 32, 83 with 64 x 64; 1 token by 4099 x 4095 13.0 with 64 x 32 in four
+// splits, which the rule takes, 11.4 in two, 14.8 with 64 x 64 in one.
 struct W8AnyCost {
     int bo, bt;
     float fixed, step;             // us per tile, and for each 128 k
@@ -105,8 +106,9 @@ inline W8Plan w8_plan_fast(int64_t T, int64_t n, int64_t m) {
         const double groups = (double)w8_cdiv(w8_cdiv(m, 16) * w8_cdiv(T, 16), 256);
         const double one = 16e-3 * (double)n * (1.0 + 0.36 * (T < 16 ? T : 16) / 16.0) / 19.5;
         const double t = 1.9 + groups * one + 0.12 * (double)w8_cdiv(n, 1024);
-        // turns of 8 waves x 128 k; of 256 k where they come out even on long rows (1 token:
-        // 8192 x 8192 14.8 against 15.7 us, but 5120 x 5120 12.5 against 10.3)
+        // turns of 8 waves x 128 k; of 256 k where they come out even on long rows (1 token by 8192 x
+        // 8192: 14.7 against 15.8 us; 4096 x 8192 8.7 / 9.4; 4096 x 16384 13.8 / 23.2; 4096 x 14336
+        // and 8192 x 10240 the same; 2048 x 8192 7.9 / 7.6; but 5120 x 5120 12.6 / 10.3)
         if (t < least) best = w8_split(n >= 8192 && n % 2048 == 0 ? W8_ROW4 : W8_ROW2, n, 1, 64);
     }
     return best;

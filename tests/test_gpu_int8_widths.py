@@ -57,3 +57,16 @@ def test_norm_in_place(pwq, d, which, dtype, gdt):
     assert torch.equal(dst, h) and all(torch.equal(got[k], want[k]) for k in want)
     g = None if G is None else f64(G)
     check_codes(got, O.rms_norm_quantize(f64(h), g, 1e-5), exact=False, y=O.rms_norm(f64(h), g, 1e-5))
+
+
+@pytest.mark.parametrize("d", [2048, 40000])
+def test_norm_past_127_times_float32(pwq, d):
+    """One value and a gain that carry y past what a float32 scale can hold: an infinite scale, codes 0."""
+    X = torch.zeros(3, d, device=DEV)
+    X[:, 5] = 1.0
+    X[1] = 1.0
+    G = torch.full((d,), 3e38, device=DEV)
+    r = pwq.rms_norm_quantize(X, G, eps=0.0, want_sums=True)
+    q, s, n = O.rms_norm_quantize(f64(X), f64(G), 0.0)
+    assert (np.isinf(s[[0, 2]]).all() and not q[[0, 2]].any()) == (d == 40000) and np.isfinite(s[1])
+    check_codes(r, (q, s, n), exact=True)
