@@ -25,11 +25,11 @@
 // Layout: NT threads per row (whole waves), NC chunks of 8 consecutive elements per thread: few
 // threads with several chunks, so that a compute unit has several rows in flight and one's loads
 // run beside another's stores.  Rows too long for the registers are read again for the second
-// step.  Measured (kernel trace, operands cold): norm of 8192 x 8192 bf16 with a residual 95 us (4.9
-// TB/s, as a copy of as many bytes), in float32 178 (4.9), with a float32 gain 99, rows that start
-// at any byte 131; token quantizer of 4096 x 28672 bf16 80 us (4.4 TB/s), float32 112 (5.3), with a
-// channel scale 114-127 (the scales, twice X's bytes, are loaded from L2 and divided by for every
-// row); one row of 8192 4.7 us, an empty launch 2.2.
+// step.  Measured (kernel trace, operands cold): norm of 8192 x 8192 bf16 with a residual 96 us (4.9
+// TB/s, as a copy of as many bytes), in float32 183 (4.8), with a float32 gain 102, rows that start
+// at any byte 137; token quantizer of 4096 x 28672 bf16 81 us (4.4 TB/s), float32 112 (5.2), with a
+// channel scale 122 (the scales, twice X's bytes, are loaded from L2 and divided by for every row);
+// one row of 8192 4.8 us, an empty launch 2.2.
 #pragma once
 
 #include "../../include/pwq.h"
@@ -657,11 +657,11 @@ hipError_t tok_pick(const TokArgs& a, hipStream_t s) {
     if (d <= 8192) return tok_go<XT, 256, 4, MODE, AL>(a, s);
     // Longer rows: as far as the registers hold them (the norm holds x, r and g at once, the float64
     // products the gains beside h, unaligned rows the shifted chunks), since a row read twice takes
-    // longer: token quantizer 80 us at 4096 x 28672, 125 at 28671, which is read twice; norm with a
-    // residual 176 at 28672 against 250 at 32768.  The norm of 16-bit rows in seven chunks is the one
-    // that spills (8 registers of a lane: 20 % more bytes written at 28672 wide, by the counters) and
-    // is still ahead.  Rows between the steps pay for the chunks they leave empty: norm of 4096 rows
-    // of 16384 / 18944 / 20480 / 24576 / 28672: 107 / 139 / 142 / 161 / 176 us.
+    // longer: token quantizer 81 us at 4096 x 28672, 129 at 28671, which is read twice; norm with a
+    // residual 177 at 28672 against 250 at 32768.  The norm of 16-bit rows in seven chunks is the one
+    // that spills (8 registers of a lane: 67 MB more written over 4096 rows, 19 % at 28672 wide) and is
+    // still ahead.  Rows between the steps pay for the chunks they leave empty: norm of 4096 rows
+    // of 16384 / 18944 / 20480 / 24576 / 28672: 103 / 132 / 137 / 160 / 177 us.
     if constexpr (AL == ROWS_VEC || MODE != TOK_NORM64) {
         if (d <= 16384) return tok_go<XT, 512, 4, MODE, AL>(a, s);
     }

@@ -199,15 +199,15 @@ __device__ __forceinline__ void w8_out4(const W8Args& a, i32x4 acc, int64_t t, i
 //           with KG = 1 and a fourth stage: 64 tokens by 28672 x 8192 42 against 46 us, 2048 by
 //           768 x 768 6.1 against 6.8, though 2048 by 1008 x 4096 16.0 against 14.5).
 //
-// Measured (kernel trace, operands cold): 8192^3 440-445 us, 8192 tokens by 28672 x 8192 1540-1640 us
-// (2.3-2.5 POP/s).  The clock falls to 1.83 and 1.63 GHz there, which is what power leaves of 2.4, and
-// the matrix units are busy 64 and 69 % of its cycles.  512 tokens by 8192 x 8192 41 us, 36 with the
+// Measured (kernel trace, operands cold): 8192^3 440-463 us, 8192 tokens by 28672 x 8192 1550-1640 us
+// (2.3-2.5 POP/s).  The clock falls to 1.84 and 1.60 GHz there, which is what power leaves of 2.4, and
+// the matrix units are busy 65 and 69 % of its cycles.  512 tokens by 8192 x 8192 41 us, 36 with the
 // operands in the last cache (128 x 128 tiles, one per compute unit: 130 KB through LDS per 128 k
 // are 1024 cycles at 128 bytes each, twice the multiplies', and the matrix units are busy 41 % of
 // the time); 48 tokens by 28672 x 8192 43-45 us (5.3-5.6 TB/s of codes); one token by 8192 x 28672
 // 41-43 us and 4.6 for the join (5.4-5.7 TB/s without it).  Between 17 and 512 tokens the tiles are
-// far from both bounds: 64 by 8192 x 8192 26 us (the codes alone 11), 192 by 28672 x 8192 71 (41), 256
-// by 17920 x 5120 47 (21), 320 by 28672 x 8192 102 (68): tiles padded with tokens that are not
+// far from both bounds: 64 by 8192 x 8192 28 us (the codes alone 11), 192 by 28672 x 8192 69 (41), 256
+// by 17920 x 5120 46 (21), 320 by 28672 x 8192 98 (68): tiles padded with tokens that are not
 // there, and too few of them for the chip.
 // Stages of 64 k at KG = 2, which would fit 128 x 128 and 128 x 256 tiles, move 64-byte pieces of
 // rows and take 30 % longer.
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(512) void w8_tile_kernel(W8Args a) {
 // less often gain); there with zero-points and float32 outputs 16.  Loads of the words around
 // them, moved down by 0 to 3 bytes, were 1 to 5 % faster there and 10 % slower at few tokens, as
 // they are five.  Long prompts are 2 to 3 times as long as on aligned rows (2000 tokens by 28671 x
-// 8191: 1040 us; 2048 by 28672 x 8192: 444), more than copying both operands to aligned rows
+// 8191: 1040 us; 2048 by 28672 x 8192: 460), more than copying both operands to aligned rows
 // would cost; with 128 x 128 tiles the symmetric form needs 258 registers, two too many for a
 // second workgroup on a compute unit, the zero-point form 248.
 
