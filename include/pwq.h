@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define PWQ_ABI_VERSION 6
+#define PWQ_ABI_VERSION 7
 
 typedef enum pwq_status {
     PWQ_OK = 0,
@@ -495,6 +495,75 @@ pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_i
                                      const int32_t* x_sums, const void* codes, const uint16_t* scales,
                                      const uint16_t* zeros, int64_t d_out, void* Y, int y_dtype, int64_t ldy, void* ws,
                                      size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit floating point
+ * A layer whose weights and activations are e4m3 codes (8 bits: sign, 4 of exponent, 3 of mantissa;
+ * largest value 448, no infinities, 0x7f and 0xff NaN) with a scale for each block of 128: one per
+ * 128 x 128 weights, one per 128 values of a token ([MQM] "Affine Quantization" with Z = 0 and
+ * "Group-wise Quantization", with floating codes).  Per block with largest magnitude top:
+ *   PWQ_SCALE_F32   s = float32(top / 448); below 2^-120 it counts as 0
+ *   PWQ_SCALE_E8M0  s = 2^n, n >= -127 the least with top <= 448 2^n; stored as the byte n + 127,
+ *                   255 is NaN
+ *   code = the e4m3 value nearest to y / s (the exact quotient), ties to even; s = 0 gives code 0.
+ * A block with a value that is not finite gets scale NaN and codes 0, so that products with it come
+ * out NaN.  The last block of a row or column may be partial.
+ *
+ * pwq_quantize_tokens_fp8:
+ *   X       n_tok x d, x_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldx.
+ *   codes   n_tok x d bytes, leading dimension ldq.
+ *   scales  groups x n_tok (groups = d / 128, rounded up), leading dimension lds >= n_tok: float32 or
+ *           bytes, by scale_type.  Groups come first because the product reads one group's scales of
+ *           neighbouring tokens.
+ * pwq_quantize_blocks_fp8: n_mats matrices W (a layer, or a stack of experts' layers)
+ *   W       d_out x d_in each, w_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldw; stride_w
+ *           elements (at least d_out ldw) between two matrices.
+ *   codes   n_mats x d_out x d_in bytes, dense; scales n_mats x (d_out / 128) x (d_in / 128), both
+ *           rounded up, dense.
+ * In all four calls PWQ_EINVAL where an output shares a byte with an input or with another output. */
+typedef enum pwq_scale_type {
+    PWQ_SCALE_F32 = 0,
+    PWQ_SCALE_E8M0 = 1
+} pwq_scale_type;
+pwq_status pwq_quantize_tokens_fp8(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx, int scale_type,
+                                   uint8_t* codes, int64_t ldq, void* scales, int64_t lds, void* stream);
+pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, int64_t d_out, int64_t d_in, int64_t ldw,
+                                   int64_t stride_w, int scale_type, uint8_t* codes, void* scales, void* stream);
+
+/* pwq_quantized_matmul_fp8:
+ *   Y[t][o] = sum over blocks b of x_scales[b][t] * scales[o / 128][b] * sum over k in b of
+ *             X[t][k] codes[o][k]
+ *   X         n_tok x d_in e4m3 codes, leading dimension ldx; x_scales groups x n_tok, leading
+ *             dimension lds; codes d_out x d_in, dense; scales (d_out / 128) x groups, dense: the
+ *             formats above, both scales of scale_type.
+ *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy.
+ *   ws        pwq_quantized_matmul_fp8_workspace_size(n_tok, d_in, d_out) bytes, 16-byte aligned (0
+ *             bytes: ws may be NULL): the float32 sums of a split k.
+ * Any alignment and sizes; rows of X and codes that start at multiples of 16 bytes take the faster
+ * kernels.  Codes of NaN and scales of NaN give NaN.
+ *
+ * pwq_quantized_matmul_fp8_grouped: the product of a layer of experts.  n_rows output rows are sorted
+ * by expert: those of expert e are offsets[e] .. offsets[e + 1] - 1, any number of them.
+ *   Y[i] = X[rows[i]] times expert e's weights, X[i] without rows
+ *   X         n_x x d_in; x_scales groups x n_x, leading dimension lds.  Without rows n_x = n_rows.
+ *   codes     n_experts x d_out x d_in, scales n_experts x (d_out / 128) x groups, dense.
+ *   offsets   DEVICE int32[n_experts + 1], not decreasing, 0 .. n_rows.  What lies outside is taken as
+ *             the nearer end; of experts whose rows overlap, either may write them.
+ *   rows      optional DEVICE int32[n_rows], 0 .. n_x - 1, one row as often as wanted.  Another index
+ *             gives a row of NaN.
+ *   Y         n_rows x d_out; rows before offsets[0] and from offsets[n_experts] on are left alone.
+ *   ws        pwq_quantized_matmul_fp8_grouped_workspace_size(n_rows, d_in, d_out, n_experts) bytes.
+ * PWQ_EINVAL when Y needs more tiles of 64 x 64 than one launch holds (2^23).  Calls that may run at
+ * the same time need a ws each. */
+size_t pwq_quantized_matmul_fp8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out);
+pwq_status pwq_quantized_matmul_fp8(const uint8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const void* x_scales,
+                                    int64_t lds, int scale_type, const uint8_t* codes, const void* scales, int64_t d_out,
+                                    void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+size_t pwq_quantized_matmul_fp8_grouped_workspace_size(int64_t n_rows, int64_t d_in, int64_t d_out, int64_t n_experts);
+pwq_status pwq_quantized_matmul_fp8_grouped(const uint8_t* X, int64_t n_x, int64_t d_in, int64_t ldx, const void* x_scales,
+                                            int64_t lds, int scale_type, const uint8_t* codes, const void* scales,
+                                            int64_t d_out, int64_t n_experts, const int32_t* offsets, const int32_t* rows,
+                                            int64_t n_rows, void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                                            void* stream);
 
 #ifdef __cplusplus
 }

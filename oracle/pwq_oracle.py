@@ -132,7 +132,8 @@ __all__ = [
     "storage_bytes", "asym_scale_zero", "quantize_codes_asym", "rtn_asym", "dequant_asym",
     "pack_uint4", "unpack_uint4", "quantized_matmul", "tensor_scales", "channel_abs_mean",
     "awq_scales", "awq_search", "quantize_tokens", "rms_norm", "rms_norm_quantize",
-    "quantized_matmul_int8",
+    "quantized_matmul_int8", "e4m3_values", "e8m0_values", "quantize_tokens_fp8", "quantize_blocks_fp8",
+    "quantized_matmul_fp8", "quantized_matmul_fp8_grouped",
 ]
 
 
@@ -700,6 +701,109 @@ def quantized_matmul_int8(X: np.ndarray, x_scales: np.ndarray, codes: np.ndarray
         c = c - np.asarray(zeros, dtype=np.float64).reshape(-1, 1)
     s = np.asarray(X, dtype=np.float64) @ c.T
     return s * np.asarray(scales, dtype=np.float64).reshape(1, -1) * np.asarray(x_scales, dtype=np.float64).reshape(-1, 1)
+
+
+# ------------------------------------------------------------------ 8-bit floating point
+# Codes are e4m3 bytes (sign, 4 bits of exponent, 3 of mantissa, 0x7f NaN), scales float32 or e8m0
+# bytes (2^(b - 127), 255 NaN), one for each block of 128.
+
+def e4m3_values(codes: np.ndarray) -> np.ndarray:
+    """float64 values of e4m3 bytes."""
+    b = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    e, m = (b >> 3) & 15, b & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v = np.where((b & 127) == 127, np.nan, v)
+    return np.where(b & 128, -v, v)
+
+
+def e8m0_values(scales: np.ndarray) -> np.ndarray:
+    """float64 values of e8m0 bytes; float32 scales as they are."""
+    s = np.asarray(scales)
+    if s.dtype != np.uint8:
+        return s.astype(np.float64)
+    return np.where(s == 255, np.nan, 2.0 ** (s.astype(np.float64) - 127.0))
+
+
+def _e4m3_scale(top: float, e8m0: bool):
+    """The stored scale of a block whose largest magnitude is `top`."""
+    if not e8m0:
+        if not np.isfinite(top):
+            return np.float32(np.nan)
+        s = np.float32(top / 448.0)
+        return np.float32(0.0) if s < np.float32(2.0 ** -120) else s
+    if not np.isfinite(top):
+        return np.uint8(255)
+    n = -127
+    while top > 448.0 * 2.0 ** n:
+        n += 1
+    return np.uint8(n + 127)
+
+
+def _e4m3_codes(y: np.ndarray, scale) -> np.ndarray:
+    """e4m3 bytes nearest to y / scale (float64), ties to the even byte; zeros for a scale 0 or NaN."""
+    s = float(e8m0_values(np.asarray(scale)))
+    if not s > 0.0:
+        return np.zeros(y.shape, dtype=np.uint8)
+    q = np.abs(y) / s
+    v = e4m3_values(np.arange(127))
+    i = np.searchsorted(v, q, side="right") - 1               # v[i] <= q
+    j = np.minimum(i + 1, 126)
+    mid = (v[i] + v[j]) / 2
+    up = (q > mid) | ((q == mid) & (i % 2 == 1))
+    return np.where(up, j, i).astype(np.uint8) | np.where(np.signbit(y), 128, 0).astype(np.uint8)
+
+
+def quantize_tokens_fp8(X: np.ndarray, e8m0: bool = False):
+    """(codes, scales) of X, tokens x d: a scale per token and 128 values, scales as groups x tokens."""
+    X = np.asarray(X, dtype=np.float64)
+    T, d = X.shape
+    G = -(-d // 128)
+    codes = np.zeros((T, d), dtype=np.uint8)
+    scales = np.zeros((G, T), dtype=np.uint8 if e8m0 else np.float32)
+    for t in range(T):
+        for g in range(G):
+            y = X[t, 128 * g:128 * g + 128]
+            scales[g, t] = _e4m3_scale(np.max(np.abs(y)), e8m0)
+            codes[t, 128 * g:128 * g + 128] = _e4m3_codes(y, scales[g, t])
+    return codes, scales
+
+
+def quantize_blocks_fp8(W: np.ndarray, e8m0: bool = False):
+    """(codes, scales) of W, one matrix or a stack of them: a scale per 128 x 128."""
+    W = np.asarray(W, dtype=np.float64)
+    if W.ndim == 3:
+        parts = [quantize_blocks_fp8(w, e8m0) for w in W]
+        return np.stack([c for c, _ in parts]), np.stack([s for _, s in parts])
+    m, d = W.shape
+    codes = np.zeros((m, d), dtype=np.uint8)
+    scales = np.zeros((-(-m // 128), -(-d // 128)), dtype=np.uint8 if e8m0 else np.float32)
+    for i in range(scales.shape[0]):
+        for j in range(scales.shape[1]):
+            at = np.s_[128 * i:128 * i + 128, 128 * j:128 * j + 128]
+            scales[i, j] = _e4m3_scale(np.max(np.abs(W[at])), e8m0)
+            codes[at] = _e4m3_codes(W[at], scales[i, j])
+    return codes, scales
+
+
+def quantized_matmul_fp8(X: np.ndarray, x_scales: np.ndarray, codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """float64 sum over k of (x_scales X)[t, k] (scales codes)[o, k]."""
+    d, m = X.shape[1], codes.shape[0]
+    x = e4m3_values(X) * np.repeat(e8m0_values(x_scales).T, 128, axis=1)[:, :d]
+    w = e4m3_values(codes) * np.repeat(np.repeat(e8m0_values(scales), 128, axis=0)[:m], 128, axis=1)[:, :d]
+    return x @ w.T
+
+
+def quantized_matmul_fp8_grouped(X: np.ndarray, x_scales: np.ndarray, codes: np.ndarray, scales: np.ndarray,
+                                 offsets, rows=None, out: Optional[np.ndarray] = None) -> np.ndarray:
+    """Rows offsets[e] .. offsets[e + 1] - 1 of `out` (zeros if not given) from expert e's weights."""
+    n = len(rows) if rows is not None else X.shape[0]
+    Y = np.zeros((n, codes.shape[1])) if out is None else np.array(out, dtype=np.float64)
+    for e in range(codes.shape[0]):
+        i = np.arange(offsets[e], offsets[e + 1])
+        r = i if rows is None else np.asarray(rows)[i]
+        if len(i):
+            Y[i] = quantized_matmul_fp8(X[r], x_scales[:, r], codes[e], scales[e])
+    return Y
 
 
 # ------------------------------------------------------------------ error measures

@@ -25,6 +25,8 @@ pwq_status hip_status(hipError_t e) {
 constexpr int64_t MAX_DIM = (int64_t)1 << 30;
 
 bool bad_dim(int64_t v) { return v < 0 || v > MAX_DIM; }
+constexpr int64_t F8_MAX_EXPERTS = 65536;
+constexpr int64_t F8_MAX_VALUES = (int64_t)1 << 40;    // weights of all experts together
 constexpr int64_t QMM_MAX_COLS = (int64_t)1 << 24;     // ldx (>= d_in) of the quantized product
 
 bool group_ok(int32_t g, int64_t d_in) {
@@ -568,6 +570,105 @@ pwq_status pwq_quantized_matmul_int8(const int8_t* X, int64_t n_tok, int64_t d_i
     if (outputs_overlap(out, in)) return PWQ_EINVAL;
     return hip_status(w8_launch(X, n_tok, d_in, ldx, x_scales, zeros ? x_sums : nullptr, (const uint8_t*)codes, scales,
                                 zeros, d_out, Y, y_dtype, ldy, ws, (hipStream_t)stream));
+}
+
+// ------------------------------------------------------------------ 8-bit floating point
+static bool scale_type_ok(int t) { return t == PWQ_SCALE_F32 || t == PWQ_SCALE_E8M0; }
+static int64_t scale_size(int t) { return t == PWQ_SCALE_F32 ? 4 : 1; }
+
+pwq_status pwq_quantize_tokens_fp8(const void* X, int x_dtype, int64_t n_tok, int64_t d, int64_t ldx, int scale_type,
+                                   uint8_t* codes, int64_t ldq, void* scales, int64_t lds, void* stream) {
+    if (!float_dtype(x_dtype) || !scale_type_ok(scale_type)) return PWQ_EDTYPE;
+    if (bad_dim(n_tok) || d < 1 || bad_dim(d) || ldx < d || bad_dim(ldx) || ldq < d || bad_dim(ldq) || lds < n_tok ||
+        bad_dim(lds))
+        return PWQ_EINVAL;
+    if (n_tok == 0) return PWQ_OK;
+    if (!X || !codes || !scales || !aligned(X, float_size(x_dtype)) || !aligned(scales, scale_size(scale_type)))
+        return PWQ_EINVAL;
+    const Rows out[] = {rows_of(codes, n_tok, d, ldq, 1), rows_of(scales, cdiv(d, 128), n_tok, lds, scale_size(scale_type))};
+    const Rows in[] = {rows_of(X, n_tok, d, ldx, float_size(x_dtype))};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
+    return hip_status(f8_tokens_launch(X, x_dtype, n_tok, d, ldx, scale_type == PWQ_SCALE_E8M0, codes, ldq, scales, lds,
+                                       (hipStream_t)stream));
+}
+
+pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, int64_t d_out, int64_t d_in, int64_t ldw,
+                                   int64_t stride_w, int scale_type, uint8_t* codes, void* scales, void* stream) {
+    if (!float_dtype(w_dtype) || !scale_type_ok(scale_type)) return PWQ_EDTYPE;
+    if (n_mats < 0 || n_mats > F8_MAX_EXPERTS || bad_dim(d_out) || d_in < 1 || bad_dim(d_in) || ldw < d_in || bad_dim(ldw))
+        return PWQ_EINVAL;
+    if (n_mats == 0 || d_out == 0) return PWQ_OK;
+    if (n_mats > 1 && (stride_w < d_out * ldw || stride_w > F8_MAX_VALUES)) return PWQ_EINVAL;
+    if (d_out > F8_MAX_VALUES / n_mats / d_in) return PWQ_EINVAL;
+    if (!W || !codes || !scales || !aligned(W, float_size(w_dtype)) || !aligned(scales, scale_size(scale_type)))
+        return PWQ_EINVAL;
+    const int64_t e = float_size(w_dtype), span = (n_mats - 1) * (n_mats > 1 ? stride_w : 0) + (d_out - 1) * ldw + d_in;
+    const Rows out[] = {bytes_of(codes, n_mats * d_out * d_in),
+                        bytes_of(scales, n_mats * cdiv(d_out, 128) * cdiv(d_in, 128) * scale_size(scale_type))};
+    const Rows in[] = {n_mats > 1 ? bytes_of(W, span * e) : rows_of(W, d_out, d_in, ldw, e)};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
+    return hip_status(f8_blocks_launch(W, w_dtype, n_mats, d_out, d_in, ldw, stride_w, scale_type == PWQ_SCALE_E8M0, codes,
+                                       scales, (hipStream_t)stream));
+}
+
+// Both products: n_rows rows of Y from n_x rows of X; offsets and rows NULL for one matrix
+static bool fp8_dims_ok(int64_t n_rows, int64_t d_in, int64_t d_out, int64_t n_experts) {
+    return !bad_dim(n_rows) && d_in >= 1 && !bad_dim(d_in) && !bad_dim(d_out) && n_experts >= 1 && n_experts <= F8_MAX_EXPERTS;
+}
+static size_t fp8_workspace(int64_t n_rows, int64_t d_in, int64_t d_out, int64_t n_experts) {
+    if (!fp8_dims_ok(n_rows, d_in, d_out, n_experts) || n_rows == 0 || d_out == 0 || !f8_size_ok(n_rows, d_out, n_experts))
+        return 0;
+    return f8_ws_bytes(n_rows, d_in, d_out, n_experts);
+}
+static pwq_status fp8_matmul(F8Call c, int scale_type, size_t ws_bytes, void* stream) {
+    if (!float_dtype(c.y_dtype) || !scale_type_ok(scale_type)) return PWQ_EDTYPE;
+    if (!fp8_dims_ok(c.T, c.n, c.m, c.experts) || bad_dim(c.xrows) || c.ldx < c.n || bad_dim(c.ldx) || c.ldsx < c.xrows ||
+        bad_dim(c.ldsx) || c.ldy < c.m || bad_dim(c.ldy))
+        return PWQ_EINVAL;
+    if (c.T == 0 || c.m == 0) return PWQ_OK;
+    if (!f8_size_ok(c.T, c.m, c.experts) || c.m > F8_MAX_VALUES / c.experts / c.n) return PWQ_EINVAL;
+    if ((c.rows ? c.xrows < 1 : c.xrows != c.T) || !c.X || !c.sx || !c.C || !c.sw || !c.Y) return PWQ_EINVAL;
+    const int64_t ss = scale_size(scale_type);
+    if (!aligned(c.sx, ss) || !aligned(c.sw, ss) || !aligned(c.offsets, 4) || !aligned(c.rows, 4) ||
+        !aligned(c.Y, float_size(c.y_dtype)))
+        return PWQ_EINVAL;
+    const size_t need = fp8_workspace(c.T, c.n, c.m, c.experts);
+    if (need && (!c.ws || ws_bytes < need || !aligned(c.ws, 16))) return PWQ_EWORKSPACE;
+    const int64_t groups = cdiv(c.n, 128);
+    const Rows out[] = {rows_of(c.Y, c.T, c.m, c.ldy, float_size(c.y_dtype)), bytes_of(need ? c.ws : nullptr, (int64_t)need)};
+    const Rows in[] = {rows_of(c.X, c.xrows, c.n, c.ldx, 1), rows_of(c.sx, groups, c.xrows, c.ldsx, ss),
+                       bytes_of(c.C, c.experts * c.m * c.n), bytes_of(c.sw, c.experts * cdiv(c.m, 128) * groups * ss),
+                       bytes_of(c.offsets, 4 * (c.experts + 1)), bytes_of(c.rows, 4 * c.T)};
+    if (outputs_overlap(out, in)) return PWQ_EINVAL;
+    c.e8 = scale_type == PWQ_SCALE_E8M0;
+    return hip_status(f8_launch(c, (hipStream_t)stream));
+}
+
+size_t pwq_quantized_matmul_fp8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out) {
+    return fp8_workspace(n_tok, d_in, d_out, 1);
+}
+
+pwq_status pwq_quantized_matmul_fp8(const uint8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const void* x_scales,
+                                    int64_t lds, int scale_type, const uint8_t* codes, const void* scales, int64_t d_out,
+                                    void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    return fp8_matmul(F8Call{X, x_scales, codes, scales, nullptr, nullptr, Y, ws, n_tok, ldx, lds, ldy, n_tok, d_in, d_out, 1,
+                             y_dtype, false},
+                      scale_type, ws_bytes, stream);
+}
+
+size_t pwq_quantized_matmul_fp8_grouped_workspace_size(int64_t n_rows, int64_t d_in, int64_t d_out, int64_t n_experts) {
+    return fp8_workspace(n_rows, d_in, d_out, n_experts);
+}
+
+pwq_status pwq_quantized_matmul_fp8_grouped(const uint8_t* X, int64_t n_x, int64_t d_in, int64_t ldx, const void* x_scales,
+                                            int64_t lds, int scale_type, const uint8_t* codes, const void* scales,
+                                            int64_t d_out, int64_t n_experts, const int32_t* offsets, const int32_t* rows,
+                                            int64_t n_rows, void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                                            void* stream) {
+    if (n_rows > 0 && d_out > 0 && !offsets) return PWQ_EINVAL;
+    return fp8_matmul(F8Call{X, x_scales, codes, scales, offsets, rows, Y, ws, n_x, ldx, lds, ldy, n_rows, d_in, d_out,
+                             n_experts, y_dtype, false},
+                      scale_type, ws_bytes, stream);
 }
 
 }  // extern "C"

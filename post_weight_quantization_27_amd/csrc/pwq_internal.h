@@ -102,6 +102,30 @@ hipError_t w8_launch(const int8_t* X, int64_t T, int64_t n, int64_t ldx, const f
                      const uint8_t* C, const uint16_t* sw, const uint16_t* zeros, int64_t m, void* Y, int y_dtype,
                      int64_t ldy, void* ws, hipStream_t s);
 
+// e4m3 codes with a scale per block of 128 (e8: scales are powers of two in 8 bits).
+hipError_t f8_tokens_launch(const void* X, int x_dtype, int64_t T, int64_t d, int64_t ldx, bool e8, uint8_t* Q, int64_t ldq,
+                            void* S, int64_t lds, hipStream_t s);
+hipError_t f8_blocks_launch(const void* W, int w_dtype, int64_t mats, int64_t m, int64_t d, int64_t ldw, int64_t stride,
+                            bool e8, uint8_t* Q, void* S, hipStream_t s);
+
+// Y = X C^T on e4m3 codes; with offsets, C's matrix by the rows' expert and X's rows by `rows`.
+struct F8Call {
+    const uint8_t* X;
+    const void* sx;
+    const uint8_t* C;
+    const void* sw;
+    const int32_t* offsets;
+    const int32_t* rows;
+    void* Y;
+    void* ws;
+    int64_t xrows, ldx, ldsx, ldy, T, n, m, experts;       // X's rows; Y's rows, d_in, d_out
+    int y_dtype;
+    bool e8;
+};
+bool f8_size_ok(int64_t T, int64_t m, int64_t experts);
+size_t f8_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts);
+hipError_t f8_launch(const F8Call& c, hipStream_t s);
+
 // Reconstruction MSE.
 size_t mse_ws_bytes(int64_t n_tok, int64_t d_in, int64_t d_out);
 // the split product of the Hessian-route MSE (layers of >= 256 output tiles of 256 x 256):

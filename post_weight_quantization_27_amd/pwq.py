@@ -85,6 +85,17 @@ _SIGS = {
     "pwq_quantized_matmul_int8": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                                  _c_void_p, _i64, _c_void_p, ctypes.c_int, _i64, _c_void_p, _sz,
                                                  _c_void_p]),
+    "pwq_quantize_tokens_fp8": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int, _c_void_p, _i64,
+                                               _c_void_p, _i64, _c_void_p]),
+    "pwq_quantize_blocks_fp8": (ctypes.c_int, [_c_void_p, ctypes.c_int, _i64, _i64, _i64, _i64, _i64, ctypes.c_int,
+                                               _c_void_p, _c_void_p, _c_void_p]),
+    "pwq_quantized_matmul_fp8_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "pwq_quantized_matmul_fp8": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _i64, ctypes.c_int, _c_void_p,
+                                                _c_void_p, _i64, _c_void_p, ctypes.c_int, _i64, _c_void_p, _sz, _c_void_p]),
+    "pwq_quantized_matmul_fp8_grouped_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
+    "pwq_quantized_matmul_fp8_grouped": (ctypes.c_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _i64, ctypes.c_int,
+                                                        _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64,
+                                                        _c_void_p, ctypes.c_int, _i64, _c_void_p, _sz, _c_void_p]),
     "pwq_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "pwq_profile_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_int64), ctypes.c_int]),
@@ -640,6 +651,159 @@ def quantized_matmul_int8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.
     _check("pwq_quantized_matmul_int8", _on(
         X, L.pwq_quantized_matmul_int8, X.data_ptr(), T, d_in, ldx, sx, n, codes.data_ptr(), sw, z, m, out.data_ptr(),
         _CODES.get(out.dtype, -1), ldy, w, nb))
+    return out
+
+
+# ------------------------------------------------------------------ 8-bit floating point
+_E4M3 = torch.float8_e4m3fn
+_SCALES = {torch.float32: 0, torch.float8_e8m0fnu: 1}
+
+
+def _dense(t: torch.Tensor, name: str, dtypes, dev, shape) -> int:
+    """Address of a contiguous tensor of `shape` on dev."""
+    if t.dtype not in dtypes or t.device != dev or t.shape != shape or not t.is_contiguous():
+        _bad(name, f"contiguous {tuple(shape)} of {' / '.join(map(str, dtypes))} on {dev}")
+    return t.data_ptr()
+
+
+def _fp8_outputs(o: dict, codes_shape, scales_shape, scale_dtype, dev):
+    """(codes, scales) of o, made where missing."""
+    if scale_dtype not in _SCALES:
+        _bad("scale_dtype", "torch.float32 or torch.float8_e8m0fnu")
+    if o.get("codes") is None:
+        o["codes"] = torch.empty(codes_shape, dtype=_E4M3, device=dev)
+    if o.get("scales") is None:
+        o["scales"] = torch.empty(scales_shape, dtype=scale_dtype, device=dev)
+    return o["codes"], o["scales"]
+
+
+def quantize_tokens_fp8(X: torch.Tensor, scale_dtype=torch.float32, out: Optional[dict] = None) -> dict:
+    """e4m3 codes of activations with a scale per token and 128 values: {codes (tokens x d,
+    float8_e4m3fn), scales (d / 128 rounded up x tokens, ``scale_dtype``: float32, or float8_e8m0fnu
+    for powers of two)}.  ``out`` may hold tensors to write into."""
+    dev = X.device
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    ldx = _pitch(X, "X", _CODES, dev)
+    T, d = X.shape
+    G = -(-d // 128)
+    o = out if out is not None else {}
+    if o.get("scales") is not None:
+        scale_dtype = o["scales"].dtype
+    q, s = _fp8_outputs(o, (T, d), (G, T), scale_dtype, dev)
+    ldq = _pitch(q, "codes", (_E4M3,), dev, (T, d))
+    lds = _pitch(s, "scales", (scale_dtype,), dev, (G, T))
+    _check("pwq_quantize_tokens_fp8", _on(X, lib().pwq_quantize_tokens_fp8, X.data_ptr(), _CODES[X.dtype], T, d, ldx,
+                                          _SCALES[scale_dtype], q.data_ptr(), ldq, s.data_ptr(), lds))
+    return o
+
+
+def quantize_blocks_fp8(W: torch.Tensor, scale_dtype=torch.float32, out: Optional[dict] = None) -> dict:
+    """e4m3 codes of weights with a scale per 128 x 128 of them: {codes (W's shape, float8_e4m3fn),
+    scales (W's last two sizes / 128, rounded up; ``scale_dtype`` as in quantize_tokens_fp8)}.  W is a
+    matrix (d_out x d_in) or a stack of them (experts x d_out x d_in).  ``out`` may hold contiguous
+    tensors to write into."""
+    dev = W.device
+    if dev.type != "cuda":
+        _bad("W", "a GPU tensor")
+    if W.dim() not in (2, 3) or W.dtype not in _CODES:
+        _bad("W", "a matrix or a stack of matrices of " + " / ".join(map(str, _CODES)))
+    E = W.shape[0] if W.dim() == 3 else 1
+    m, d = W.shape[-2:]
+    ldw, stride = d, m * d
+    if W.numel():
+        ldw = _pitch(W if W.dim() == 2 else W[0], "W", _CODES, dev)
+        stride = W.stride(0) if W.dim() == 3 and E > 1 else m * ldw
+    o = out if out is not None else {}
+    if o.get("scales") is not None:
+        scale_dtype = o["scales"].dtype
+    shape = (*W.shape[:-2], -(-m // 128), -(-d // 128))
+    q, s = _fp8_outputs(o, W.shape, shape, scale_dtype, dev)
+    _dense(q, "codes", (_E4M3,), dev, W.shape)
+    _dense(s, "scales", (scale_dtype,), dev, shape)
+    _check("pwq_quantize_blocks_fp8", _on(W, lib().pwq_quantize_blocks_fp8, W.data_ptr(), _CODES[W.dtype], E, m, d, ldw,
+                                          stride, _SCALES[scale_dtype], q.data_ptr(), s.data_ptr()))
+    return o
+
+
+def _fp8_x(X: torch.Tensor, x_scales: torch.Tensor, dev):
+    """(pitch of X, pitch of its scales, scale type)"""
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    ldx = _pitch(X, "X", (_E4M3,), dev)
+    T, d = X.shape
+    return ldx, _pitch(x_scales, "x_scales", _SCALES, dev, (-(-d // 128), T)), _SCALES[x_scales.dtype]
+
+
+def _fp8_ws(ws, need: int, dev):
+    """(address, bytes) of the workspace"""
+    if not need:
+        return None, 0
+    if ws is None:
+        ws = _ws(need, dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _bad("ws", f"contiguous bytes on {dev}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def quantized_matmul_fp8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                         out_dtype=torch.float16, out: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X What^T on e4m3 codes with a scale per block of 128: X, x_scales from quantize_tokens_fp8,
+    codes, scales from quantize_blocks_fp8 (both scales of one type)."""
+    dev = X.device
+    ldx, lds, st = _fp8_x(X, x_scales, dev)
+    T, d = X.shape
+    if codes.dim() != 2:
+        _bad("codes", f"d_out x {d}")
+    m = codes.shape[0]
+    c = _dense(codes, "codes", (_E4M3,), dev, (m, d))
+    sw = _dense(scales, "scales", (x_scales.dtype,), dev, (-(-m // 128), -(-d // 128)))
+    ldy = m
+    if out is None:
+        out = torch.empty(T, m, dtype=out_dtype, device=dev)
+    else:
+        ldy = _pitch(out, "out", _CODES, dev, (T, m))
+    L = lib()
+    ws, nb = _fp8_ws(ws, L.pwq_quantized_matmul_fp8_workspace_size(T, d, m), dev)
+    _check("pwq_quantized_matmul_fp8", _on(
+        X, L.pwq_quantized_matmul_fp8, X.data_ptr(), T, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, out.data_ptr(),
+        _CODES.get(out.dtype, -1), ldy, ws.data_ptr() if nb else None, nb))
+    return out
+
+
+def quantized_matmul_fp8_grouped(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                                 offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, out_dtype=torch.float16,
+                                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """quantized_matmul_fp8 with one of several weight matrices for each row: codes (experts x d_out x
+    d_in) and scales from quantize_blocks_fp8 of the stack.  Output rows offsets[e] .. offsets[e + 1] - 1
+    (int32 on the GPU, experts + 1 of them) multiply expert e's.  ``rows`` (int32 on the GPU): row i
+    reads row rows[i] of X, so that X need not hold a token once per expert; without it, row i of X.
+    Rows of ``out`` before the first expert's and behind the last one's are left as they are (of a new
+    tensor: whatever memory held)."""
+    dev = X.device
+    ldx, lds, st = _fp8_x(X, x_scales, dev)
+    n_x, d = X.shape
+    if codes.dim() != 3:
+        _bad("codes", f"experts x d_out x {d}")
+    E, m = codes.shape[:2]
+    c = _dense(codes, "codes", (_E4M3,), dev, (E, m, d))
+    sw = _dense(scales, "scales", (x_scales.dtype,), dev, (E, -(-m // 128), -(-d // 128)))
+    off = _vec(offsets, "offsets", (torch.int32,), dev, E + 1)
+    T, r = n_x, None
+    if rows is not None:
+        T = rows.shape[0] if rows.dim() else 0
+        r = _vec(rows, "rows", (torch.int32,), dev, T)
+    ldy = m
+    if out is None:
+        out = torch.empty(T, m, dtype=out_dtype, device=dev)
+    else:
+        ldy = _pitch(out, "out", _CODES, dev, (T, m))
+    L = lib()
+    ws, nb = _fp8_ws(ws, L.pwq_quantized_matmul_fp8_grouped_workspace_size(T, d, m, E), dev)
+    _check("pwq_quantized_matmul_fp8_grouped", _on(
+        X, L.pwq_quantized_matmul_fp8_grouped, X.data_ptr(), n_x, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, E, off, r,
+        T, out.data_ptr(), _CODES.get(out.dtype, -1), ldy, ws.data_ptr() if nb else None, nb))
     return out
 
 

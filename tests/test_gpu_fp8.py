@@ -1,0 +1,518 @@
+"""GPU parity of the 8-bit floating point calls against the float64 oracle: the token and block
+quantizers, the product with a scale per block of 128, the product grouped by expert, and the four
+together.
+
+Bars.  Quantizers: codes and scales equal to the last bit (the code is that of the exact quotient).
+Products, with S = the sum of |x_scale scale x w| over k of an output: the float16 instructions (every
+float32 output) hold exact products in float32 sums of at most 128 terms a block, then one scale
+product, one multiply-add a block and one addition a split of k, each off by at most a whole step
+2^-23 of the sum so far: (128 + blocks + 16) 2^-23 S.  The e4m3 instruction (16-bit outputs) keeps of
+each eight consecutive products what is at least 2^-13 of the largest one's power of two, so it loses
+less than 8 * 2^-13 of the largest product of each eight; that comes on top, and half a step of the
+output's type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+SCALES = {"f32": torch.float32, "e8m0": torch.float8_e8m0fnu}
+
+
+@pytest.fixture(scope="module")
+def pwq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from post_weight_quantization_27_amd import pwq as P
+    P.lib()
+    return P
+
+
+def half_step(y, dtype):
+    a = np.abs(y)
+    mant, emin = {torch.float32: (24, -126), torch.float16: (11, -14), torch.bfloat16: (8, -126)}[dtype]
+    e = np.maximum(np.floor(np.log2(np.maximum(a, 1e-300))), emin)
+    return 2.0 ** (e - mant)
+
+
+def raw(t):
+    """A tensor's stored values: bytes of the 8-bit types."""
+    return (t.contiguous().view(torch.uint8) if t.element_size() == 1 else t).cpu().numpy()
+
+
+def e4m3(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV).view(torch.float8_e4m3fn)
+
+
+def as_scales(a):
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    return t.view(torch.float8_e8m0fnu) if a.dtype == np.uint8 else t
+
+
+def hidden(rng, T, d, dtype):
+    x = rng.standard_normal((T, d)) * np.where(rng.random(d) < 0.02, 20.0, 1.0)
+    return torch.from_numpy(x.astype(np.float32)).to(TYPES[dtype]).to(DEV)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check_codes(r, want):
+    torch.cuda.synchronize()
+    q, s = want
+    gs = raw(r["scales"])
+    assert gs.dtype == s.dtype and np.array_equal(gs, s, equal_nan=s.dtype != np.uint8)
+    assert np.array_equal(raw(r["codes"]), q)
+
+
+# ------------------------------------------------------------------ quantizers
+@pytest.mark.parametrize("scales", list(SCALES))
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,d", [(1, 1), (3, 5), (1, 8), (2, 127), (5, 128), (17, 129), (1, 8192), (40, 768), (33, 1031), (300, 200)])
+def test_tokens(pwq, T, d, dtype, scales):
+    rng = np.random.default_rng(T * 1000 + d)
+    x = hidden(rng, T, d, dtype)
+    check_codes(pwq.quantize_tokens_fp8(x, scale_dtype=SCALES[scales]), O.quantize_tokens_fp8(f64(x), scales == "e8m0"))
+
+
+@pytest.mark.parametrize("scales", list(SCALES))
+def test_tokens_strided(pwq, scales):
+    rng = np.random.default_rng(8)
+    T, d = 21, 264
+    big = hidden(rng, T, 3 * d, "bf16")
+    for off in (0, 8, 3):
+        x = big[:, off:off + d]
+        want = O.quantize_tokens_fp8(f64(x), scales == "e8m0")
+        codes = torch.full((T, d + 9), 7, dtype=torch.uint8, device=DEV)
+        s = torch.full((3, T + 5), 7, dtype=torch.uint8, device=DEV)
+        s = s.view(torch.float8_e8m0fnu) if scales == "e8m0" else torch.full((3, T + 5), 7.0, device=DEV)
+        r = pwq.quantize_tokens_fp8(x, out={"codes": codes.view(torch.float8_e4m3fn)[:, off:off + d], "scales": s[:, :T]})
+        check_codes(r, want)
+        assert (codes[:, :off] == 7).all() and (codes[:, off + d:] == 7).all() and (raw(s[:, T:]) == 7).all()
+
+
+def special_rows():
+    """Blocks that are hard to round: ties, borders, tiny and huge values, zeros, NaN and infinities."""
+    rng = np.random.default_rng(1)
+    v = O.e4m3_values(np.arange(127))
+    mid = (v[1:] + v[:-1]) / 2
+    rows = []
+    for s in (1.0, 2.0 ** -30, 0.75, 1.0 / 3, 1.7e30, 2.0 ** -119.5, 1.1 * 2.0 ** -120):
+        s = float(np.float32(s))
+        for shift in (-1, 0, 1):                       # the float32 beside, on, and beyond the middles
+            x = np.float32(mid * s)
+            x = np.nextafter(x, np.float32(shift * np.inf)) if shift else x
+            rows.append(np.concatenate([[np.float32(448.0 * s)], x * rng.choice([-1, 1], x.size)]).astype(np.float32))
+    for top in (0.0, -0.0, 2.0 ** -149, 447 * 2.0 ** -120, 448 * 2.0 ** -120, 2.0 ** -126, 3.4e38, np.nan, np.inf, -np.inf,
+                448.0, np.nextafter(np.float32(448.0), np.float32(500)), 2.0 ** -112 * 1.75, 2.0 ** -118 * 1.75):
+        x = np.zeros(127, dtype=np.float32)
+        x[:64] = rng.standard_normal(64) * 2.0 ** -20
+        x[5] = top
+        x[:64] = np.clip(x[:64], -abs(top), abs(top)) if np.isfinite(top) else x[:64]
+        rows.append(x)
+    return np.stack(rows).astype(np.float32)
+
+
+@pytest.mark.parametrize("scales", list(SCALES))
+def test_special_blocks(pwq, scales):
+    x = special_rows()
+    e8 = scales == "e8m0"
+    check_codes(pwq.quantize_tokens_fp8(torch.from_numpy(x).to(DEV), scale_dtype=SCALES[scales]), O.quantize_tokens_fp8(x, e8))
+    W = np.zeros((len(x), 128, 128), dtype=np.float32)
+    W[:, 77, :127] = x                                    # each row as a block of its own
+    check_codes(pwq.quantize_blocks_fp8(torch.from_numpy(W).to(DEV), scale_dtype=SCALES[scales]), O.quantize_blocks_fp8(W, e8))
+
+
+@pytest.mark.parametrize("scales", list(SCALES))
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(1, 1), (3, 7), (128, 128), (130, 300), (257, 1031), (2, 100, 136), (3, 129, 63)])
+def test_blocks(pwq, shape, dtype, scales):
+    rng = np.random.default_rng(sum(shape))
+    w = hidden(rng, int(np.prod(shape[:-1])), shape[-1], dtype).view(shape)
+    check_codes(pwq.quantize_blocks_fp8(w, scale_dtype=SCALES[scales]), O.quantize_blocks_fp8(f64(w), scales == "e8m0"))
+
+
+def test_blocks_strided(pwq):
+    rng = np.random.default_rng(3)
+    big = hidden(rng, 4 * 150, 400, "f16").view(4, 150, 400)
+    for w in (big[1:3, 5:140, 16:280], big[:, :131, 3:3 + 257], big[2, 7:]):
+        check_codes(pwq.quantize_blocks_fp8(w), O.quantize_blocks_fp8(f64(w)))
+    out = {"codes": torch.empty(2, 135, 264, dtype=torch.float8_e4m3fn, device=DEV),
+           "scales": torch.empty(2, 2, 3, dtype=torch.float8_e8m0fnu, device=DEV)}
+    assert pwq.quantize_blocks_fp8(big[1:3, 5:140, 16:280], out=out) is out
+    check_codes(out, O.quantize_blocks_fp8(f64(big[1:3, 5:140, 16:280]), True))
+
+
+# ------------------------------------------------------------------ products
+def random_codes(rng, *shape):
+    """Codes as a quantizer makes them of normal values, a few of every other kind."""
+    v = np.clip(rng.standard_normal(shape) * 100, -448, 448).astype(np.float32)
+    q = torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    some = rng.random(shape) < 0.02
+    b = rng.integers(0, 256, shape).astype(np.uint8)
+    b[(b & 127) == 127] = 0x7e
+    return np.where(some, b, q).astype(np.uint8)
+
+
+def random_scales(rng, e8, *shape):
+    if e8:
+        return rng.integers(110, 130, shape).astype(np.uint8)
+    return (rng.random(shape) * 0.02 + 1e-4).astype(np.float32)
+
+
+def bounds(X, sx, C, sw, want, out_dtype):
+    """How far each output may be (see the top of this file)."""
+    d, m = X.shape[1], C.shape[0]
+    x = np.abs(O.e4m3_values(X)) * np.repeat(O.e8m0_values(sx).T, 128, axis=1)[:, :d]
+    w = np.abs(O.e4m3_values(C)) * np.repeat(np.repeat(O.e8m0_values(sw), 128, axis=0)[:m], 128, axis=1)[:, :d]
+    x, w = np.nan_to_num(x), np.nan_to_num(w)
+    S = x @ w.T
+    tol = (128 + -(-d // 128) + 16) * 2.0 ** -23 * S + half_step(want, out_dtype) * 1.0001
+    if out_dtype != torch.float32:
+        for k in range(0, d, 8):
+            top = np.zeros_like(S)
+            for i in range(k, min(k + 8, d)):
+                np.maximum(top, np.outer(x[:, i], w[:, i]), out=top)
+            tol += 2.0 ** -10 * top
+    return tol
+
+
+def check_product(got, X, sx, C, sw, out_dtype):
+    torch.cuda.synchronize()
+    want = O.quantized_matmul_fp8(X, sx, C, sw)
+    g = f64(got)
+    assert np.array_equal(np.isnan(g), np.isnan(want))
+    tol = bounds(X, sx, C, sw, np.nan_to_num(want), out_dtype)
+    if out_dtype == torch.float16:                        # past its range: infinities
+        big = np.abs(want) > 65504
+        assert np.all(np.isinf(g[big & (np.abs(want) > 65520 * 1.01)]))
+        g, want = np.where(big, 0, g), np.where(big, 0, want)
+    with np.errstate(invalid="ignore"):
+        off = np.nan_to_num(np.abs(g - want)) - tol
+    assert np.all(off <= 0), (np.max(off), np.unravel_index(np.argmax(off), off.shape))
+
+
+PRODUCTS = [(1, 1, 1), (2, 5, 3), (1, 16, 17), (3, 128, 128), (5, 130, 129), (1, 768, 768), (17, 144, 200), (64, 256, 64),
+            (65, 384, 300), (33, 1601, 203), (130, 1040, 515), (300, 777, 131), (16, 4096, 160), (257, 512, 272)]
+
+
+@pytest.mark.parametrize("scales", list(SCALES))
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("T,n,m", PRODUCTS)
+def test_product(pwq, T, n, m, out, scales):
+    rng = np.random.default_rng(T * 7 + n + m)
+    X, C = random_codes(rng, T, n), random_codes(rng, m, n)
+    G, e8 = -(-n // 128), scales == "e8m0"
+    sx, sw = random_scales(rng, e8, G, T), random_scales(rng, e8, -(-m // 128), G)
+    got = pwq.quantized_matmul_fp8(e4m3(X), as_scales(sx), e4m3(C), as_scales(sw), out_dtype=TYPES[out])
+    check_product(got, X, sx, C, sw, TYPES[out])
+
+
+@pytest.mark.parametrize("n", [512, 333])
+def test_product_strided(pwq, n):
+    rng = np.random.default_rng(n)
+    T, m = 37, 150
+    G = -(-n // 128)
+    X, C = random_codes(rng, T, n), random_codes(rng, m, n)
+    sx, sw = random_scales(rng, False, G, T), random_scales(rng, False, 2, G)
+    for pad, out in ((16, torch.bfloat16), (3, torch.float32)):
+        wide = torch.full((T, n + pad), 127, dtype=torch.uint8, device=DEV)          # NaN codes around
+        wide[:, pad // 2:pad // 2 + n] = torch.from_numpy(X).to(DEV)
+        s = torch.full((G, T + 6), float("nan"), device=DEV)
+        s[:, :T] = torch.from_numpy(sx).to(DEV)
+        Y = torch.full((T, m + 7), 7.0, dtype=out, device=DEV)
+        pwq.quantized_matmul_fp8(wide.view(torch.float8_e4m3fn)[:, pad // 2:pad // 2 + n], s[:, :T], e4m3(C), as_scales(sw),
+                                 out=Y[:, :m])
+        check_product(Y[:, :m], X, sx, C, sw, out)
+        assert (Y[:, m:] == 7).all()
+
+
+@pytest.mark.parametrize("n,out", [(640, "bf16"), (640, "f32"), (643, "f16")])
+def test_nan_codes_and_scales(pwq, n, out):
+    rng = np.random.default_rng(n)
+    T, m = 70, 140
+    G = -(-n // 128)
+    X, C = random_codes(rng, T, n), random_codes(rng, m, n)
+    sx, sw = random_scales(rng, False, G, T), random_scales(rng, False, 2, G)
+    X[3, n - 1], C[100, 0], sx[2, 66] = 0x7f, 0xff, np.nan
+    sx[1, 5] = 0.0
+    got = pwq.quantized_matmul_fp8(e4m3(X), as_scales(sx), e4m3(C), as_scales(sw), out_dtype=TYPES[out])
+    check_product(got, X, sx, C, sw, TYPES[out])
+    assert torch.isnan(got[3]).all() and torch.isnan(got[66]).all() and torch.isnan(got[:, 100]).all()
+    assert int(torch.isnan(got).sum()) == 2 * m + (T - 2)
+    sw[1, 0] = np.nan
+    got = pwq.quantized_matmul_fp8(e4m3(X), as_scales(sx), e4m3(C), as_scales(sw), out_dtype=TYPES[out])
+    assert torch.isnan(got[:, 128:]).all() and not torch.isnan(got[0, :100]).any()
+    e8x, e8w = random_scales(rng, True, G, T), random_scales(rng, True, 2, G)
+    e8x[0, 9], e8w[0, 1] = 255, 255
+    got = pwq.quantized_matmul_fp8(e4m3(X), as_scales(e8x), e4m3(C), as_scales(e8w), out_dtype=TYPES[out])
+    assert torch.isnan(got[9]).all() and torch.isnan(got[:, :128]).all() and not torch.isnan(got[10, 128:]).any()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_e8m0_extremes(pwq, out):
+    """Scales from 2^-127 to 2^127 whose products are ordinary numbers."""
+    T, n, m = 18, 256, 130
+    rng = np.random.default_rng(4)
+    X, C = random_codes(rng, T, n), random_codes(rng, m, n)
+    for a, b in ((0, 254), (254, 0), (1, 250), (127, 127), (60, 180)):
+        sx, sw = np.full((2, T), a, dtype=np.uint8), np.full((2, 2), b, dtype=np.uint8)
+        got = pwq.quantized_matmul_fp8(e4m3(X), as_scales(sx), e4m3(C), as_scales(sw), out_dtype=TYPES[out])
+        check_product(got, X, sx, C, sw, TYPES[out])
+
+
+def test_empty(pwq):
+    q = torch.empty(0, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    c = torch.zeros(64, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    assert pwq.quantized_matmul_fp8(q, torch.empty(2, 0, device=DEV), c, torch.ones(1, 2, device=DEV)).shape == (0, 64)
+    r = pwq.quantize_tokens_fp8(torch.empty(0, 300, device=DEV))
+    assert r["codes"].shape == (0, 300) and r["scales"].shape == (3, 0)
+    assert pwq.quantize_blocks_fp8(torch.empty(0, 300, device=DEV))["scales"].shape == (0, 3)
+    assert pwq.quantize_blocks_fp8(torch.empty(0, 5, 300, device=DEV))["codes"].shape == (0, 5, 300)
+    off = torch.zeros(2, dtype=torch.int32, device=DEV)
+    y = pwq.quantized_matmul_fp8_grouped(q, torch.empty(2, 0, device=DEV), c[None], torch.ones(1, 1, 2, device=DEV), off)
+    assert y.shape == (0, 64)
+
+
+def test_offsets_past_32_bits(pwq):
+    """Weights of more than 2^31 bytes, outputs at more than 2^32 bytes: the last rows and columns."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    n, m, T = 32768, 70000, 3
+    C = torch.randint(0, 0x70, (m, n), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    X = torch.randint(0, 0x70, (T, n), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    sx, sw = torch.rand(256, T, device=DEV, generator=g), torch.rand(547, 256, device=DEV, generator=g)
+    y = pwq.quantized_matmul_fp8(X, sx, C, sw, out_dtype=torch.float32)
+    rows = list(range(0, m, 9973)) + [m - 1]
+    x64 = O.e4m3_values(raw(X)) * np.repeat(raw(sx).astype(np.float64).T, 128, axis=1)
+    c64 = O.e4m3_values(raw(C[rows])) * np.repeat(raw(sw).astype(np.float64)[[r // 128 for r in rows]], 128, axis=1)
+    want = x64 @ c64.T                                    # every term positive: S is the value itself
+    assert np.all(np.abs(f64(y[:, rows]) - want) <= (128 + 256 + 17) * 2.0 ** -23 * want)
+    T, m = 140000, 16384                                  # 140000 x 16384 in 16 bits: 4.6 GB
+    X = torch.randint(0, 0x70, (T, 128), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    C = torch.randint(0, 0x70, (m, 128), dtype=torch.uint8, device=DEV, generator=g).view(torch.float8_e4m3fn)
+    sx, sw = torch.rand(1, T, device=DEV, generator=g) * 1e-3, torch.rand(128, 1, device=DEV, generator=g)
+    y = pwq.quantized_matmul_fp8(X, sx, C, sw, out_dtype=torch.bfloat16)
+    at = torch.tensor([0, 1, 131071, T - 1], device=DEV)
+    check_product(y[at], raw(X[at]), raw(sx[:, at]), raw(C), raw(sw), torch.bfloat16)
+
+
+# ------------------------------------------------------------------ grouped
+def routed(rng, counts, first=0, behind=0):
+    off = np.concatenate([[0], np.cumsum(counts)]) + first
+    return off.astype(np.int32), int(off[-1]) + behind
+
+
+GROUPED = [  # counts per expert, d_in, d_out, rows before the first expert, rows behind the last
+    ([3], 128, 128, 0, 0),
+    ([1, 0, 2], 256, 130, 0, 0),
+    ([0, 0, 0], 256, 64, 0, 5),
+    ([5, 16, 0, 17, 1, 64], 384, 200, 0, 3),
+    ([70, 1, 0, 0, 129, 300], 256, 136, 4, 9),
+    ([7, 33, 2], 333, 77, 2, 1),
+    ([1] * 70 + [0] * 60 + [2] * 70, 160, 48, 0, 0),
+    ([0] * 130 + [40], 128, 32, 1, 0),
+]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("out,scales", [("f32", "f32"), ("bf16", "f32"), ("f16", "e8m0"), ("f32", "e8m0")])
+@pytest.mark.parametrize("case", range(len(GROUPED)))
+def test_grouped(pwq, case, out, scales, gather):
+    counts, n, m, first, behind = GROUPED[case]
+    rng = np.random.default_rng(case * 10 + gather)
+    off, T = routed(rng, counts, first, behind)
+    E, G, e8 = len(counts), -(-n // 128), scales == "e8m0"
+    n_x = 11 if gather else T
+    rows = rng.integers(0, n_x, T).astype(np.int32) if gather else None
+    X, C = random_codes(rng, n_x, n), random_codes(rng, E, m, n)
+    sx, sw = random_scales(rng, e8, G, n_x), random_scales(rng, e8, E, -(-m // 128), G)
+    Y = torch.full((T, m + 3), 7.0, dtype=TYPES[out], device=DEV)
+    pwq.quantized_matmul_fp8_grouped(e4m3(X), as_scales(sx), e4m3(C), as_scales(sw), torch.from_numpy(off).to(DEV),
+                                     rows=None if rows is None else torch.from_numpy(rows).to(DEV), out=Y[:, :m])
+    torch.cuda.synchronize()
+    assert (Y[:, m:] == 7).all() and (Y[:first] == 7).all() and (Y[int(off[-1]):] == 7).all()
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if b > a:
+            r = np.arange(a, b) if rows is None else rows[a:b]
+            check_product(Y[a:b, :m], X[r], sx[:, r], C[e], sw[e], TYPES[out])
+
+
+def test_grouped_bad_indexes_and_offsets(pwq):
+    """Rows with an index outside X are NaN; offsets outside Y are taken as its ends; nothing else changes."""
+    rng = np.random.default_rng(6)
+    n, m, E, T, n_x = 256, 72, 3, 40, 5
+    X, C = random_codes(rng, n_x, n), random_codes(rng, E, m, n)
+    sx, sw = random_scales(rng, False, 2, n_x), random_scales(rng, False, E, 1, 2)
+    rows = rng.integers(0, n_x, T).astype(np.int32)
+    bad = [2, 19, 39]
+    rows[bad] = [-1, n_x, 2 ** 31 - 1]
+    buf = torch.full((T + 2, m), 7.0, dtype=torch.bfloat16, device=DEV)
+    args = (e4m3(X), as_scales(sx), e4m3(C), as_scales(sw))
+    for off in ([0, 10, 25, 40], [-5, 10, 25, 2000], [-2 ** 31, 10, 25, 2 ** 31 - 1]):
+        buf.fill_(7.0)
+        Y = pwq.quantized_matmul_fp8_grouped(*args, torch.tensor(off, dtype=torch.int32, device=DEV),
+                                             rows=torch.from_numpy(rows).to(DEV), out=buf[1:-1])
+        assert torch.isnan(Y[bad]).all() and int(torch.isnan(Y).sum()) == 3 * m
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+        ends = [0, 10, 25, 40]
+        for e in range(E):
+            i = np.array([t for t in range(ends[e], ends[e + 1]) if t not in bad])
+            check_product(Y[i], X[rows[i]], sx[:, rows[i]], C[e], sw[e], torch.bfloat16)
+    # decreasing: an expert without rows; the others' are right
+    buf.fill_(7.0)
+    Y = pwq.quantized_matmul_fp8_grouped(*args, torch.tensor([0, 30, 20, 20], dtype=torch.int32, device=DEV),
+                                         rows=torch.from_numpy(np.abs(rows) % n_x).to(DEV), out=buf[1:-1])
+    r = (np.abs(rows) % n_x)[:30]
+    check_product(Y[:30], X[r], sx[:, r], C[0], sw[0], torch.bfloat16)
+    assert (Y[30:] == 7).all()
+
+
+# ------------------------------------------------------------------ as they are used
+def _layer(pwq, rng, E, n, m, st):
+    W = torch.from_numpy((rng.standard_normal((E, m, n)) * 0.05).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    return W, pwq.quantize_blocks_fp8(W, scale_dtype=SCALES[st])
+
+
+@pytest.mark.parametrize("st", list(SCALES))
+def test_a_mixture_of_experts_layer(pwq, st):
+    """Two tokens' worth of rows per expert through both projections, from float weights and back."""
+    rng = np.random.default_rng(12)
+    T, top, E, n, h = 37, 2, 6, 384, 264
+    x = hidden(rng, T, n, "bf16")
+    W1, q1 = _layer(pwq, rng, E, n, h, st)
+    W2, q2 = _layer(pwq, rng, E, h, n, st)
+    expert = np.stack([rng.permutation(E)[:top] for _ in range(T)])
+    weight = rng.random((T, top)).astype(np.float32)
+    order = np.argsort(expert.ravel(), kind="stable")
+    off = np.concatenate([[0], np.cumsum(np.bincount(expert.ravel(), minlength=E))]).astype(np.int32)
+    offsets, rows = torch.from_numpy(off).to(DEV), torch.from_numpy((order // top).astype(np.int32)).to(DEV)
+    a = pwq.quantize_tokens_fp8(x, scale_dtype=SCALES[st])
+    y1 = pwq.quantized_matmul_fp8_grouped(a["codes"], a["scales"], q1["codes"], q1["scales"], offsets, rows=rows,
+                                          out_dtype=torch.bfloat16)
+    act = torch.nn.functional.silu(y1.float()).to(torch.bfloat16)
+    b = pwq.quantize_tokens_fp8(act, scale_dtype=SCALES[st])
+    y2 = pwq.quantized_matmul_fp8_grouped(b["codes"], b["scales"], q2["codes"], q2["scales"], offsets, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    # each step against the oracle on that step's own inputs
+    check_codes(a, O.quantize_tokens_fp8(f64(x), st == "e8m0"))
+    check_codes(b, O.quantize_tokens_fp8(f64(act), st == "e8m0"))
+    r = order // top
+    for e in range(E):
+        i = np.arange(off[e], off[e + 1])
+        check_product(y1[i], raw(a["codes"])[r[i]], raw(a["scales"])[:, r[i]], raw(q1["codes"])[e], raw(q1["scales"])[e],
+                      torch.bfloat16)
+        check_product(y2[i], raw(b["codes"])[i], raw(b["scales"])[:, i], raw(q2["codes"])[e], raw(q2["scales"])[e],
+                      torch.float32)
+    # the layer's output, near the float layer's: four factors off by at most 2^-4 (3.6 % rms), two of
+    # them in each sum of many terms of random sign
+    got, want = np.zeros((T, n)), np.zeros((T, n))
+    y2 = f64(y2)
+    for i, j in enumerate(order):
+        t, k = divmod(j, top)
+        got[t] += weight[t, k] * y2[i]
+        z = f64(x)[t] @ f64(W1[expert[t, k]]).T
+        want[t] += weight[t, k] * ((z / (1 + np.exp(-z))) @ f64(W2[expert[t, k]]).T)
+    assert np.linalg.norm(got - want) < 0.2 * np.linalg.norm(want)
+
+
+def test_one_expert_is_the_plain_product(pwq):
+    rng = np.random.default_rng(9)
+    for n, m, T in ((512, 300, 45), (333, 77, 20)):
+        W, q = _layer(pwq, rng, 1, n, m, "f32")
+        a = pwq.quantize_tokens_fp8(hidden(rng, T, n, "f16"))
+        for out in TYPES.values():
+            one = pwq.quantized_matmul_fp8(a["codes"], a["scales"], q["codes"][0], q["scales"][0], out_dtype=out)
+            off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+            y = pwq.quantized_matmul_fp8_grouped(a["codes"], a["scales"], q["codes"], q["scales"], off, out_dtype=out)
+            assert torch.allclose(one.float(), y.float(), rtol=2 ** -7 if out != torch.float32 else 1e-5, atol=1e-3)
+
+
+def test_graphs_and_streams(pwq):
+    """The chain captured and replayed on new inputs, routing among them, with eager calls between; two
+    streams at once, each with a workspace of its own."""
+    rng = np.random.default_rng(20)
+    T, E, n, m = 48, 5, 640, 272
+    W, q = _layer(pwq, rng, E, n, m, "f32")
+    x = hidden(rng, T, n, "bf16")
+    off = torch.tensor([0, 10, 10, 30, 41, 48], dtype=torch.int32, device=DEV)
+    a = {"codes": torch.empty(T, n, dtype=torch.float8_e4m3fn, device=DEV), "scales": torch.empty(5, T, device=DEV)}
+    y, z = torch.zeros(T, m, dtype=torch.bfloat16, device=DEV), torch.zeros(T, m, device=DEV)
+
+    def ws_of(P):
+        need = max(P.lib().pwq_quantized_matmul_fp8_grouped_workspace_size(T, n, m, E),
+                   P.lib().pwq_quantized_matmul_fp8_workspace_size(T, n, m), 16)
+        return torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def chain(a, y, z, ws):
+        pwq.quantize_tokens_fp8(x, out=a)
+        pwq.quantized_matmul_fp8_grouped(a["codes"], a["scales"], q["codes"], q["scales"], off, out=y, ws=ws)
+        pwq.quantized_matmul_fp8(a["codes"], a["scales"], q["codes"][1], q["scales"][1], out=z, ws=ws)
+
+    ws = ws_of(pwq)
+    chain(a, y, z, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(a, y, z, ws)
+    routes = [[0, 10, 10, 30, 41, 48], [0, 0, 48, 48, 48, 48], [5, 6, 7, 8, 20, 44], [0, 1, 2, 3, 4, 5]]
+    for i, route in enumerate(routes):
+        x.copy_(hidden(rng, T, n, "bf16"))
+        off.copy_(torch.tensor(route, dtype=torch.int32))
+        y.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        a2, y2, z2 = {}, torch.full_like(y, 3.0), torch.empty_like(z)
+        a2 = {k: torch.empty_like(v) for k, v in a.items()}
+        chain(a2, y2, z2, ws_of(pwq))
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(z, z2) and torch.equal(a["scales"], a2["scales"])
+        assert (y[:route[0]] == 3).all() and (y[route[-1]:] == 3).all()
+    # two streams
+    sets = [({k: torch.empty_like(v) for k, v in a.items()}, torch.full_like(y, 3.0), torch.empty_like(z), ws_of(pwq))
+            for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for s, args in zip(streams, sets):
+            with torch.cuda.stream(s):
+                chain(*args)
+    torch.cuda.synchronize()
+    for _, y2, z2, _ in sets:
+        assert torch.equal(y, y2) and torch.equal(z, z2)
+
+
+def test_binding_refuses(pwq):
+    q = torch.zeros(8, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    c = torch.zeros(3, 64, 256, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    sx, sw = torch.ones(2, 8, device=DEV), torch.ones(3, 1, 2, device=DEV)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    e8 = torch.ones(2, 8, device=DEV).to(torch.float8_e8m0fnu)
+    f = pwq.quantized_matmul_fp8
+    for args in ((q, sx.t(), c[0], sw[0]), (q, sx[:1], c[0], sw[0]), (q, e8, c[0], sw[0]), (q, sx, c, sw), (q, sx, c[0, :, :128], sw[0]),
+                 (q.view(torch.uint8), sx, c[0], sw[0]), (q, sx.cpu(), c[0], sw[0]), (q, sx.double(), c[0], sw[0])):
+        with pytest.raises(ValueError):
+            f(*args)
+    with pytest.raises(pwq.PwqError):
+        f(q, sx, c[0], sw[0], out_dtype=torch.float64)
+    g = pwq.quantized_matmul_fp8_grouped
+    for args, kw in (((q, sx, c, sw, off[:3]), {}), ((q, sx, c, sw, off.long()), {}), ((q, sx, c, sw, off.cpu()), {}),
+                     ((q, sx, c[0], sw, off), {}), ((q, sx, c, sw[:2], off), {}), ((q, sx, c, sw, off), {"rows": off.long()}),
+                     ((q, sx, c, sw, off), {"out": torch.empty(7, 64, device=DEV)})):
+        with pytest.raises(ValueError):
+            g(*args, **kw)
+    with pytest.raises(ValueError):
+        pwq.quantize_tokens_fp8(torch.zeros(4, 64, device=DEV), scale_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        pwq.quantize_tokens_fp8(torch.zeros(4, 64, device=DEV).t())
+    with pytest.raises(ValueError):
+        pwq.quantize_blocks_fp8(torch.zeros(4, 64, dtype=torch.float64, device=DEV))
+    with pytest.raises(pwq.PwqError):                       # experts between each other's rows
+        pwq.quantize_blocks_fp8(torch.zeros(64, 2, 256, device=DEV).permute(1, 0, 2))
