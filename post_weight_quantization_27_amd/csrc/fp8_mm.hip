@@ -16,6 +16,9 @@
 // A block's sum is multiplied by its two scales and added to the output's float32 sum.
 #include "../../include/pwq.h"
 #include "fp8.h"
+#include "fp8_plan.h"
+
+#include <type_traits>
 
 namespace pwq {
 
@@ -26,6 +29,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int F8_CUS = 256;                // compute units (a multiple of the 8 XCDs)
 
 struct F8Args {
     const uint8_t* X;
@@ -113,11 +118,14 @@ __device__ __forceinline__ void f8_map(const F8Args& a, int64_t bid, int& to, in
 }
 
 // ------------------------------------------------------------------ scales
+// 2^(b - 127); 0 is below the normal floats, 255 NaN
+__device__ __forceinline__ float f8_pow2(uint32_t b) {
+    return __builtin_bit_cast(float, b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+}
 template <bool E8>
 __device__ __forceinline__ float f8_get(const void* s, int64_t i) {
     if constexpr (E8) {
-        const uint32_t b = ((const uint8_t*)s)[i];       // 2^(b - 127); 0 is below the normal floats, 255 NaN
-        return __builtin_bit_cast(float, b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+        return f8_pow2(((const uint8_t*)s)[i]);
     } else {
         return ((const float*)s)[i];
     }
@@ -170,6 +178,35 @@ __device__ __forceinline__ void f8_put4(const F8Args& a, f32x4 y, int64_t t, int
         }
     }
 }
+// Two fragments' outputs in 16 bits, o0 .. o0 + 31 of the 16 rows that a wave's lanes hold (lane row
+// c: outputs 4 c .. 4 c + 3 of each fragment).  Two swaps between lane rows give row c the outputs 8 c
+// .. 8 c + 7, so that a store writes 64 bytes of a row in one piece instead of 32.
+__device__ __forceinline__ void f8_put_pair16(const F8Args& a, f32x4 y0, f32x4 y1, int64_t t, int64_t end, int64_t o0, int c,
+                                              bool bad) {
+    uint32_t even[2], odd[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const auto s = __builtin_amdgcn_permlane32_swap((uint32_t)f8_16(a, y0[2 * h]) | ((uint32_t)f8_16(a, y0[2 * h + 1]) << 16),
+                                                        (uint32_t)f8_16(a, y1[2 * h]) | ((uint32_t)f8_16(a, y1[2 * h + 1]) << 16),
+                                                        false, false);
+        const auto r = __builtin_amdgcn_permlane16_swap(s[0], s[1], false, false);
+        even[h] = r[0];
+        odd[h] = r[1];
+    }
+    const uint32_t nan = 0x7fc07fc0u;                     // a NaN in both 16-bit types
+    const uint32_t v[4] = {bad ? nan : even[0], bad ? nan : even[1], bad ? nan : odd[0], bad ? nan : odd[1]};
+    const int64_t o = o0 + 8 * c;
+    if (o >= a.m || t >= end) return;
+    uint16_t* p = (uint16_t*)a.Y + t * a.ldy + o;
+    if (o + 8 <= a.m) {
+        __builtin_memcpy(p, v, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (o + e < a.m) p[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+    }
+}
+
 // the same, or the sums over this split of k
 __device__ __forceinline__ void f8_out4(const F8Args& a, f32x4 y, int64_t t, int64_t end, int64_t o, bool bad) {
     if (o >= a.m || t >= end) return;
@@ -376,37 +413,691 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
     }
 }
 
+// ------------------------------------------------------------------ rows of 16-byte multiples
+// BO x BT tile (outputs x tokens), eight waves, a block of 128 k per stage; the codes are the row
+// operand, so that a lane ends with four consecutive outputs of one token.
+//
+// Operand rows go straight from memory into LDS (global_load_lds, 16 bytes a lane), and so do the
+// block's scales, four bytes a lane: the tokens' and behind them the outputs'.  A row's 16-byte chunk
+// c lies at f8_pos, which keeps the reads free of bank conflicts.  A lane's operand of the e4m3
+// instruction is its row's chunks c and c + 4: any order of k will do that both operands share.
+//
+// The waves work in two groups of four, one half step apart: while one group reads its fragments of
+// a stage, the other runs its matrix instructions and adds the block's sums to its outputs', with a
+// barrier between the half steps.  Each SIMD holds one wave of each group.
+//   KG = 1: both groups take every stage, each its half of the tile (WO x 8 / WO waves).
+//   KG = 2: each group takes every other stage for the whole tile (WO x 4 / WO waves), with stages of
+//           its own that its own waves copy; the two sums meet in LDS at the end.
+// NST stages: a stage's copies fly while the NST - 1 before it are used.  With two (256 x 256, whose
+// stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that the fragments
+// fit the registers; every wave starts the copies of stage s + 1 when the first group starts to read
+// stage s, by when the second has read stage s - 1, and waits for them a whole step later.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+__device__ const uint4 f8_zeros = {0u, 0u, 0u, 0u};
+
+// s_waitcnt with only the vector-memory count constrained: vmcnt <= N
+template <int N>
+__device__ __forceinline__ void f8_wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+// A buffer from `base` on, for loads at 32-bit offsets: a lane's own and one for all.  The kernels keep
+// inside the operands; the size says only that any offset will do.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00027000);
+}
+
+// One workgroup per compute unit that goes through its tiles, where the registers allow it
+template <int BO, int BT, int KG>
+constexpr bool f8_persist = KG == 1 && BO * BT < 65536;
+
+template <int BO, int BT, int NST, int WO, int KG, bool E8, bool EXACT>
+__global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
+    constexpr int BK = F8_B, NW = 8 / KG, WT = NW / WO;   // waves that share a stage
+    constexpr int FO = BO / WO / 16, FT = BT / WT / 16;
+    constexpr int FP = NST == 2 ? FO / 2 : FO;            // rows of fragments in registers at a time
+    constexpr int Q = FP * FT;                            // tiles of 16 x 16 of a part
+    constexpr int L = (BO + BT) / 8 / NW;                 // copies of 8 rows per wave and stage, and one of scales
+    constexpr bool TWO = NST == 2;
+    constexpr int SLOT = (BO + BT) * BK, ST = SLOT + NW * 256;
+    constexpr int NB = BO > F8_B ? BO / F8_B : 1;         // blocks of outputs
+    constexpr bool PERSIST = f8_persist<BO, BT, KG>;
+    static_assert(L * NW * 8 == BO + BT && BO % (NW * 8) == 0 && (L + 1) * (NST - 1) < 64 && KG * NST * ST <= 163840, "tile");
+    static_assert(BO / WO <= F8_B && BT % 64 == 0 && BT / 64 < NW, "scales");
+    static_assert(KG == 1 || (NST > 2 && FO % 2 == 0 && 8 * FO / 2 * FT * 1024 <= 2 * NST * ST), "the groups' sums fit the stages");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[KG * NST * ST];
+    const int lane = threadIdx.x & 63, wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = KG == 2 ? wave8 & 3 : wave8, grp = wave8 >> 2;
+    const int wo = wave / WT, wt = wave % WT;
+    uint8_t* const lds = smem + (KG == 2 ? grp * (NST * ST) : 0);
+    // this wave's k: from kbeg in steps of KG BK; nk of its stages, the first nfull of which end
+    // inside the rows; nmax steps for everybody
+    const int64_t kend = (blockIdx.y + 1) * a.kper < a.n ? (blockIdx.y + 1) * a.kper : a.n;
+    const int64_t kbeg = (int64_t)blockIdx.y * a.kper + (KG == 2 ? grp * BK : 0);
+    const int64_t klen = kend - kbeg;
+    const int nk = klen > 0 ? (int)((klen + KG * BK - 1) / (KG * BK)) : 0;
+    const int nfull = klen >= BK ? (int)((klen - BK) / (KG * BK)) + 1 : 0;
+    const int nmax = KG == 2 ? (int)((kend - (int64_t)blockIdx.y * a.kper + KG * BK - 1) / (KG * BK)) : nk;
+
+    // copy j of this wave: 8 rows from row0(j) on, of the codes' BO rows followed by the activations' BT;
+    // a lane brings the chunk that its position holds, from an offset (32 bits) past the operand's base.
+    // Rows past the matrices repeat the last one (their outputs are not stored).  One more copy brings
+    // 64 scales: the tokens' (slots 0 ..) or the outputs'.
+    auto row0 = [&](int j) {
+        if constexpr (TWO) {
+            // the first group brings codes, rows 0 .. 63 of both halves and then the others; the second X
+            if (wave < 4) return (wave >> 1) * 128 + (j >= 4 ? 64 : 0) + (wave & 1) * 32 + (j & 3) * 8;
+            return BO + (j >= 4 ? 128 : 0) + (wave - 4) * 32 + (j & 3) * 8;
+        }
+        return (j * NW + wave) * 8;
+    };
+    auto of_x = [&](int j) { return TWO ? grp == 1 : j * NW * 8 >= BO; };
+    const int slot = TWO ? (wave + 4) & 7 : wave;
+    const uint8_t* xbase;
+    const uint8_t* cbase;
+    __amdgpu_buffer_rsrc_t xbuf, cbuf;
+    const uint8_t* sbase;
+    int64_t sstep;
+    uint32_t off[L];
+    F8Rows at;
+    int64_t o0;
+    // The order of k is free, so tiles that live on the codes' traffic start at different k: where d_in
+    // is a multiple of 4096, rows that are read at the same k in step all come from the same few
+    // memory channels.  Large token tiles share X by k instead and start together.
+    constexpr int ROT = BT <= 128 ? 3 : 0;
+    int rot;
+    auto setup = [&](int64_t tile) {
+        int to, tt;
+        f8_map(a, tile, to, tt);
+        at = f8_rows<BT>(a, tt);
+        if (at.t0 >= at.end) return false;
+        o0 = (int64_t)to * BO;
+        rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
+        cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
+        xbase = a.X + (a.rows ? 0 : at.t0 * a.ldx) + kbeg;
+        cbuf = f8_buffer(TWO && grp == 1 ? xbase : cbase);
+        xbuf = f8_buffer(xbase);                          // two stages: a wave copies rows of one operand alone, cbuf's
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int r = row0(j) + (lane >> 3);
+            const int ch = f8_pos(r & 15, lane & 7);      // the xor undoes itself
+            if (of_x(j)) {
+                const int64_t t = at.t0 + r - BO < at.end ? at.t0 + r - BO : at.end - 1;
+                off[j] = (uint32_t)((a.rows ? f8_xrow(a, t) : t - at.t0) * a.ldx + 16 * ch);
+            } else {
+                off[j] = (uint32_t)((o0 + r < a.m ? r : a.m - 1 - o0) * a.n + 16 * ch);
+            }
+        }
+        constexpr int SB = E8 ? 1 : 4;
+        const int64_t b = kbeg / BK;
+        if (slot < BT / 64) {
+            const int64_t t = at.t0 + 64 * slot + lane < at.end ? at.t0 + 64 * slot + lane : at.end - 1;
+            sbase = (const uint8_t*)a.sx + (b * a.ldsx + f8_xrow(a, t)) * SB;
+            sstep = a.ldsx * SB;
+        } else {
+            sbase = (const uint8_t*)a.sw + f8_sw_at(a, at.expert, o0 + F8_B * (lane % NB), b) * SB;
+            sstep = SB;
+        }
+        return true;
+    };
+    // copy j of stage `it` (j = L: the scales).  END: the last stage where it ends past the rows: zeros
+    // there in both operands (a byte from elsewhere may be NaN)
+    auto copy = [&](auto end, int it, int j) {
+        constexpr bool END = decltype(end)::value;
+        uint8_t* S = lds + (it % NST) * ST;
+        const int pos = !END && ROT ? (it + rot >= nfull ? it + rot - nfull : it + rot) : it;
+        if (TWO) j = j < 4 ? j : j == 4 ? L : j - 1;          // the scales with the first four
+        if (j == L) {
+            const uint8_t* p = sbase + (int64_t)pos * KG * sstep;
+            if constexpr (E8) __builtin_amdgcn_global_load_lds((const void*)p, (lds_ptr_t)(S + SLOT + slot * 256), 1, 0, 0);
+            else __builtin_amdgcn_global_load_lds((const void*)p, (lds_ptr_t)(S + SLOT + slot * 256), 4, 0, 0);
+        } else if constexpr (END) {
+            const int64_t k = (int64_t)it * (KG * BK);
+            const int ch = f8_pos((row0(j) + (lane >> 3)) & 15, lane & 7);
+            const uint8_t* base = (of_x(j) ? xbase : cbase) + k;
+            const uint8_t* p = kbeg + k + 16 * ch < kend ? base + off[j] : (const uint8_t*)&f8_zeros;
+            __builtin_amdgcn_global_load_lds((const void*)p, (lds_ptr_t)(S + row0(j) * BK), 16, 0, 0);
+        } else {
+            if (!TWO && of_x(j))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xbuf, (lds_ptr_t)(S + row0(j) * BK), 16, (int)off[j], pos * (KG * BK), 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(cbuf, (lds_ptr_t)(S + row0(j) * BK), 16, (int)off[j], pos * (KG * BK), 0, 0);
+        }
+    };
+    using No = std::false_type;
+    using Yes = std::true_type;
+    auto copy_some = [&](int it, int from, int to) {      // copies from .. to - 1, of a stage that may not be
+        for (int j = from; j < to; ++j) {
+            if (it < nfull) copy(No{}, it, j);
+            else if (it < nk) copy(Yes{}, it, j);
+        }
+    };
+
+    f32x4 acc[FO][FT];
+    const int r = lane & 15, c = lane >> 4;
+    const uint8_t* la[2];
+    const uint8_t* lb[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int o = r * BK + 16 * f8_pos(r, 4 * h + c);
+        la[h] = lds + wo * (BO / WO) * BK + o;
+        lb[h] = lds + (BO + wt * (BT / WT)) * BK + o;
+    }
+    const uint8_t* const ls = lds + SLOT + 4 * (wt * (BT / WT) + r);
+    const uint8_t* const lw = lds + SLOT + 4 * (BT + wo * (BO / WO) / F8_B);
+    // A part of the wave's FO rows of fragments against all of its tokens, whose fragments and scales the
+    // first part reads.  `read`: what else the half step of the reads does; `during(q)`: what the other
+    // does behind matrix instruction q.
+    //
+    // Scales of powers of two go into the e4m3 instruction, which adds to the outputs' sums itself.
+    // Otherwise a tile's block sum is added AHEAD instructions after the one that makes it: a wave's vector
+    // instructions run under its own matrix instructions only in part (32 cycles an instruction alone,
+    // 40 with its four multiply-adds, 45 where the last results are waited for).  With two stages the last
+    // AHEAD of a part are added in the next half step of reads (`rest`), which has time for it.
+    constexpr bool INSIDE = E8 && !EXACT;                 // the scales are the instruction's
+    constexpr int AHEAD = 2;
+    i32x8 ft[FT];
+    uint32_t sx[FT], sw;
+    float s[FT];
+    f32x4 p[AHEAD + 1];
+    auto add = [&](int i0, int q, const f32x4& v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i0 + q / FT][q % FT][e] = __builtin_fmaf(v[e], s[q % FT], acc[i0 + q / FT][q % FT][e]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto rest = [&](int i0) {                             // of the part before the one from row i0 on
+        if constexpr (!INSIDE && TWO) {
+#pragma unroll
+            for (int q = Q - AHEAD; q < Q; ++q) add(i0 ? 0 : FO - FP, q, p[q % (AHEAD + 1)]);
+        }
+    };
+    auto step = [&](auto part, int it, auto read, auto during) {
+        constexpr int I0 = decltype(part)::value * FP;
+        const int st = (it % NST) * ST;
+        i32x8 fo[FP];
+        rest(I0);
+        if constexpr (I0 == 0) {
+#pragma unroll
+            for (int j = 0; j < FT; ++j) sx[j] = *(const uint32_t*)(ls + st + 64 * j);
+            sw = *(const uint32_t*)(lw + st);
+#pragma unroll
+            for (int j = 0; j < FT; ++j) {
+                const i32x4 u = *(const i32x4*)(lb[0] + st + j * 16 * BK), v = *(const i32x4*)(lb[1] + st + j * 16 * BK);
+                ft[j] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FP; ++i) {
+            const i32x4 u = *(const i32x4*)(la[0] + st + (I0 + i) * 16 * BK), v = *(const i32x4*)(la[1] + st + (I0 + i) * 16 * BK);
+            fo[i] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        read();
+        f8_wait_lds();
+        f16x8 ho[EXACT ? FP : 1][4], ht[EXACT ? FT : 1][4];
+        if constexpr (EXACT) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                for (int i = 0; i < FP; ++i) {
+                    asm volatile("" : "+v"(fo[i]));       // waited for above: no use of it moves up
+                    ho[i][h] = f8_half(fo[i][2 * h], fo[i][2 * h + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < FT; ++j) {
+                    asm volatile("" : "+v"(ft[j]));
+                    ht[j][h] = f8_half(ft[j][2 * h], ft[j][2 * h + 1]);
+                }
+            }
+        }
+        f8_barrier();
+        __builtin_amdgcn_s_setprio(1);
+        if constexpr (INSIDE) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                f32x4& r = acc[I0 + q / FT][q % FT];
+                r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fo[q / FT], ft[q % FT], r, 0, 0, 0, (int)sw, 0, (int)sx[q % FT]);
+                during(q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            if constexpr (I0 == 0) {
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+                    s[j] = E8 ? f8_pow2(sx[j]) * f8_pow2(sw) : __builtin_bit_cast(float, sx[j]) * __builtin_bit_cast(float, sw);
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                f32x4& r = p[q % (AHEAD + 1)];
+                r = (f32x4){0.f, 0.f, 0.f, 0.f};
+                if constexpr (EXACT) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) r = __builtin_amdgcn_mfma_f32_16x16x32_f16(ho[q / FT][h], ht[q % FT][h], r, 0, 0, 0);
+                } else {
+                    r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fo[q / FT], ft[q % FT], r, 0, 0, 0, 0, 0, 0);
+                }
+                during(q);
+                __builtin_amdgcn_sched_barrier(0);
+                if (q >= AHEAD) add(I0, q - AHEAD, p[(q - AHEAD) % (AHEAD + 1)]);
+            }
+            if constexpr (!TWO)
+#pragma unroll
+                for (int q = Q - AHEAD; q < Q; ++q) add(I0, q, p[q % (AHEAD + 1)]);
+            // the sums are added up here, and not where they are next used, behind a branch
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j) asm volatile("" : "+v"(acc[I0 + i][j]));
+        }
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
+    auto none = [](auto...) {};
+    // Copies from .. to - 1 of stage `it`, spread over a part's matrix instructions: issued together they
+    // hold up the waves for as long as their bytes take (8192^3 with scales of powers of two 357 us
+    // against 419).  Where the multiply-adds fill that half step they go with the reads instead.
+    auto together = [&](int it, int from, int to) {
+#pragma unroll
+        for (int j = from; j < to; ++j) copy(No{}, it, j);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto spread = [&](int it, int from, int to) {
+        return [&copy, it, from, to](int q) {
+#pragma unroll
+            for (int j = from; j < to; ++j)
+                if (q == (2 * (j - from) + 1) * Q / (2 * (to - from))) copy(No{}, it, j);
+        };
+    };
+    // the same of a stage that may be partial, or not there
+    auto spread_some = [&](int it, int from, int to) {
+        return [&copy_some, it, from, to](int q) {
+#pragma unroll
+            for (int j = from; j < to; ++j)
+                if (q == (2 * (j - from) + 1) * Q / (2 * (to - from))) copy_some(it, j, j + 1);
+        };
+    };
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_m;
+    int64_t tile = blockIdx.x;
+    auto next = [&] {                                     // the first stages of the next tile that has rows
+        for (; tile < tiles; tile += gridDim.x) {
+            if (!setup(tile)) continue;
+            if constexpr (TWO) {
+                copy_some(0, 0, L + 1);
+                copy_some(1, 0, grp == 0 ? 5 : L + 1);
+            } else {
+                for (int q = 0; q < NST - 1; ++q) copy_some(q, 0, L + 1);
+                if (INSIDE && (KG == 2 || grp == 1)) copy_some(NST - 1, 0, L + 1);
+            }
+            return true;
+        }
+        return false;
+    };
+    if (!next()) return;
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FO; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if constexpr (!INSIDE) {
+#pragma unroll
+            for (int q = 0; q <= AHEAD; ++q) p[q] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < FT; ++j) s[j] = 0.f;
+        }
+        if constexpr (TWO) {
+            // Quarter steps 4 s and 4 s + 2: the first group reads of stage s; 4 s + 1 and 4 s + 3: the
+            // second.  X and the scales of stage s are read by quarter 4 s + 1, the codes of the first
+            // parts by 4 s + 1, of the second by 4 s + 3.  Stage s + 2 takes their place:
+            //   codes: copies 0 .. 3 and the scales' in quarter 4 s + 3, 4 .. 7 in 4 s + 5 (with the reads
+            //   4 s + 2 and 4 s + 4); read from 4 s + 8 and 4 s + 10 on, so all but a wave's last 9 have
+            //   landed when it waits, after its instructions;
+            //   X: copies 0 .. 3 and the scales' in 4 s + 2, 4 .. 7 in 4 s + 4 (with the reads all in 4 s + 3);
+            //   read from 4 s + 8 on: the wait, in the reads of 4 s + 7, leaves 5 (ahead of the copies: 0).
+            static_assert(!TWO || (L == 8 && KG == 1 && BO == 256 && BT == 256), "two stages");
+            if (nk > 1) {
+                if (grp == 0) f8_wait_vm<5>();
+                else f8_wait_vm<9>();
+            } else {
+                f8_wait_vm<0>();
+            }
+            f8_barrier();
+            int it = 0;
+            if (grp == 0) {
+                for (; it + 2 < nfull; ++it) {
+                    if constexpr (INSIDE) step(First{}, it, none, spread(it + 1, 5, 9));
+                    else step(First{}, it, [&] { together(it + 1, 5, 9); }, none);
+                    f8_wait_vm<9>();
+                    f8_barrier();
+                    if constexpr (INSIDE) step(Second{}, it, none, spread(it + 2, 0, 5));
+                    else step(Second{}, it, [&] { together(it + 2, 0, 5); }, none);
+                    f8_wait_vm<9>();
+                    f8_barrier();
+                }
+                for (; it < nk; ++it) {
+                    step(First{}, it, [&] { copy_some(it + 1, 5, 9); }, none);
+                    f8_wait_vm<0>();
+                    f8_barrier();
+                    step(Second{}, it, [&] { copy_some(it + 2, 0, 5); }, none);
+                    f8_wait_vm<0>();
+                    f8_barrier();
+                }
+                f8_barrier();
+            } else {
+                f8_barrier();
+                for (; it + 2 < nfull; ++it) {
+                    if constexpr (INSIDE) step(First{}, it, none, spread(it + 2, 0, 5));
+                    else step(First{}, it, none, none);
+                    f8_barrier();
+                    if constexpr (INSIDE) step(Second{}, it, [] { f8_wait_vm<5>(); }, spread(it + 2, 5, 9));
+                    else step(Second{}, it, [&] { f8_wait_vm<0>(); together(it + 2, 0, 9); }, none);
+                    f8_barrier();
+                }
+                for (; it < nk; ++it) {
+                    step(First{}, it, none, none);
+                    f8_barrier();
+                    step(Second{}, it, [&] { f8_wait_vm<0>(); copy_some(it + 2, 0, 9); }, none);
+                    f8_barrier();
+                }
+            }
+        } else {
+            // KG = 1: half steps 2 s (the first group reads stage s) and 2 s + 1 (the second does).  Under
+            // its matrix instructions of stage s the first group copies stage s + NST - 1, in the place of
+            // s - 1, the second s + NST, in the place of s; with the reads both copy s + NST - 1.  Stage s + 1
+            // has landed before half step 2 s + 2: the first group waits at the end of 2 s + 1 (with the
+            // reads: of 2 s), the second in its reads of stage s: NST - 2 stages may be in flight.
+            // KG = 2: a group's own stages; under its instructions of stage s it copies s + NST and waits
+            // after them.
+            constexpr int FLY = (L + 1) * (KG == 2 && INSIDE ? NST - 1 : NST - 2);
+            auto loop = [&](auto second) {
+                constexpr bool G1 = decltype(second)::value && KG == 1;
+                constexpr int DIST = INSIDE && (G1 || KG == 2) ? NST : NST - 1;
+                int it = 0;
+                for (; it + DIST < nfull; ++it) {
+                    if constexpr (INSIDE) {
+                        step(First{}, it, [] { if (G1) f8_wait_vm<FLY>(); }, spread(it + DIST, 0, L + 1));
+                        if (!G1) f8_wait_vm<FLY>();
+                    } else {
+                        step(First{}, it, [&] { together(it + DIST, 0, L + 1); f8_wait_vm<FLY>(); }, none);
+                    }
+                    f8_barrier();
+                }
+                for (; it < nk; ++it) {
+                    if constexpr (INSIDE) {
+                        step(First{}, it, [] { if (G1) f8_wait_vm<0>(); }, spread_some(it + DIST, 0, L + 1));
+                        if (!G1) f8_wait_vm<0>();
+                    } else {
+                        step(First{}, it, [&] { copy_some(it + DIST, 0, L + 1); f8_wait_vm<0>(); }, none);
+                    }
+                    f8_barrier();
+                }
+            };
+            if (nk < NST) f8_wait_vm<0>();                    // stage 0 has landed
+            else if (INSIDE && (KG == 2 || grp == 1)) f8_wait_vm<(L + 1) * (NST - 1)>();
+            else f8_wait_vm<(L + 1) * (NST - 2)>();
+            f8_barrier();
+            if (KG == 2) {
+                if (grp == 1) f8_barrier();
+                loop(No{});
+            } else if (grp == 0) {
+                loop(No{});
+            } else {
+                f8_barrier();                                 // the second group runs half a step behind
+                loop(Yes{});
+            }
+            if (KG == 2 && nk < nmax) {                       // the other group's last stage
+                f8_barrier();
+                f8_barrier();
+            }
+            if (grp == 0) f8_barrier();                       // every wave has read its last stage
+        }
+        rest(0);
+
+        // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
+        // second; each takes the other's sums of its half from LDS
+        constexpr int FH = KG == 2 ? FO / 2 : FO;
+        if constexpr (KG == 2) {
+            f32x4* x = (f32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
+#pragma unroll
+            for (int i = 0; i < FH; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j) {
+                    const f32x4 lo = acc[i][j], hi = acc[FH + i][j];
+                    f32x4 send, keep;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        send[e] = grp == 0 ? hi[e] : lo[e];
+                        keep[e] = grp == 0 ? lo[e] : hi[e];
+                    }
+                    x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
+                    acc[i][j] = keep;
+                }
+            f8_wait_lds();
+            f8_barrier();
+#pragma unroll
+            for (int i = 0; i < FH; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
+        }
+        const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0), tb = at.t0 + wt * (BT / WT) + r;
+        const int64_t tend = at.end;
+        bool bad[FT];
+#pragma unroll
+        for (int j = 0; j < FT; ++j) bad[j] = tb + 16 * j < tend && f8_bad(a, tb + 16 * j);
+        // The next tile's first copies fly while this one's outputs are converted and stored
+        bool more = false;
+        if (PERSIST) {
+            tile += gridDim.x;
+            more = next();
+        }
+        bool stored = false;
+        if constexpr (FH % 2 == 0) {
+            if (a.splits == 1 && a.y_dtype != 0) {
+                stored = true;
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+#pragma unroll
+                    for (int i = 0; i < FH; i += 2)
+                        f8_put_pair16(a, acc[i][j], acc[i + 1][j], tb + 16 * j, tend, ob + 16 * i, c, bad[j]);
+            }
+        }
+        if (!stored) {
+#pragma unroll
+            for (int j = 0; j < FT; ++j)
+#pragma unroll
+                for (int i = 0; i < FH; ++i) f8_out4(a, acc[i][j], tb + 16 * j, tend, ob + 16 * i + 4 * c, bad[j]);
+        }
+        if (!more) break;
+    }
+}
+
+// ------------------------------------------------------------------ few tokens
+// Few tokens, where the weights are the traffic or a launch's latency counts: a workgroup owns 16
+// outputs by 16 tokens, its eight waves share k in turns of U blocks each, every lane loads its
+// fragments (16 bytes of one row) straight into registers, those of a turn while the turn before is
+// multiplied, and the waves' sums meet in LDS.  No staging: a code is used once, and X comes from L2.
+// The float16 instructions cost nothing here.  Loads past the rows or tokens take a 16-byte block of
+// zeros as their address, so none waits behind a branch.
+template <int U, bool E8>
+__global__ __launch_bounds__(512) void f8_row_kernel(F8Args a) {
+    __shared__ f32x4 red[8][64];
+    const F8Rows at = f8_rows<16>(a, blockIdx.z);
+    if (at.t0 >= at.end) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, c = lane >> 4;
+    const int64_t o0 = (int64_t)blockIdx.x * 16, t = at.t0 + r;
+    const bool xin = t < at.end;
+    const int64_t xt = f8_xrow(a, xin ? t : at.end - 1);
+    const uint8_t* crow = a.C + ((int64_t)at.expert * a.m + (o0 + r < a.m ? o0 + r : a.m - 1)) * a.n + 16 * c;
+    const uint8_t* xrow = a.X + xt * a.ldx + 16 * c;
+    const int64_t wat = f8_sw_at(a, at.expert, o0, 0);
+    const bool bad = xin && f8_bad(a, t);
+    struct Turn {
+        i32x4 co[U][2], ct[U][2];
+        float sx[U], sw[U];
+    };
+    Turn v[2];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    const int64_t left_c = a.n - 16 * c;
+    auto load = [&](Turn& q, int64_t b0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool bin = b0 + u < a.groups;
+            const int64_t b = bin ? b0 + u : 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = (b0 + u) * F8_B + 64 * h;
+                const bool in = k < left_c;
+                q.co[u][h] = __builtin_nontemporal_load((const i32x4*)(in ? crow + k : (const uint8_t*)&f8_zeros));
+                q.ct[u][h] = *(const i32x4*)(in && xin ? xrow + k : (const uint8_t*)&f8_zeros);
+            }
+            q.sx[u] = f8_get<E8>(a.sx, b * a.ldsx + xt);
+            q.sw[u] = f8_get<E8>(a.sw, wat + b);
+            if (!bin) q.sx[u] = q.sw[u] = 0.f;
+        }
+    };
+    auto mult = [&](const Turn& q) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                p = __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_half(q.co[u][h / 2][2 * (h & 1)], q.co[u][h / 2][2 * (h & 1) + 1]),
+                                                           f8_half(q.ct[u][h / 2][2 * (h & 1)], q.ct[u][h / 2][2 * (h & 1) + 1]),
+                                                           p, 0, 0, 0);
+            const float s = q.sx[u] * q.sw[u];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], s, acc[e]);
+        }
+    };
+    // turns of the whole workgroup, from a different one on each (see the tiles' order of k)
+    constexpr int TURN = 8 * U;
+    const int turns = (a.groups + TURN - 1) / TURN;
+    int turn = (int)(blockIdx.x % (unsigned)turns);
+    auto next = [&] {
+        const int64_t b0 = (int64_t)turn * TURN + wave * U;
+        turn = turn + 1 < turns ? turn + 1 : 0;
+        return b0;
+    };
+    load(v[0], next());
+    int left = turns;
+    for (; left > 2; left -= 2) {
+        load(v[1], next());
+        mult(v[0]);
+        load(v[0], next());
+        mult(v[1]);
+    }
+    if (left == 2) {
+        load(v[1], next());
+        mult(v[0]);
+        mult(v[1]);
+    } else {
+        mult(v[0]);
+    }
+    red[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) acc += red[w][lane];
+    f8_out4(a, acc, t, at.end, o0 + 4 * c, bad);
+}
+
+// ------------------------------------------------------------------ splits
+// The splits' sums of four outputs of a row at a time, in their order.  grid: x = outputs, y = rows
+__global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
+    const int64_t o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (o >= a.m) return;
+    const int64_t size = a.T * a.m;
+    int64_t t0 = 0, end = a.T;
+    if (a.offsets) {
+        t0 = a.offsets[0] < 0 ? 0 : a.offsets[0];
+        end = a.offsets[a.experts] < a.T ? a.offsets[a.experts] : a.T;
+    }
+    for (int64_t t = t0 + blockIdx.y; t < end; t += gridDim.y) {
+        const float* p = a.part + t * a.m + o;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if (o + 4 <= a.m) {
+            for (int k = 0; k < a.splits; ++k) {
+                f32x4 v;
+                __builtin_memcpy(&v, p + k * size, 16);
+                s += v;
+            }
+        } else {
+            for (int k = 0; k < a.splits; ++k)
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (o + e < a.m) s[e] += p[k * size + e];
+        }
+        f8_put4(a, s, t, o);
+    }
+}
+
 // ------------------------------------------------------------------ launches
+template <int BO, int BT, int NST, int WO, int KG, bool EXACT>
+hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
+    a.tiles_m = (int)cdiv(a.m, BO);
+    a.tiles_t = (int)f8_tiles_most(a.T, a.experts, BT);
+    const int64_t tiles = a.tiles_m * (int64_t)a.tiles_t;
+    const dim3 grid((unsigned)(f8_persist<BO, BT, KG> && tiles > F8_CUS ? F8_CUS : tiles), (unsigned)a.splits);
+    if (e8) hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, true, EXACT>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, false, EXACT>), grid, dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int U>
+hipError_t f8_row_go(const F8Args& a, bool e8, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(a.m, 16), 1, (unsigned)f8_tiles_most(a.T, a.experts, 16));
+    if (e8) hipLaunchKernelGGL((f8_row_kernel<U, true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((f8_row_kernel<U, false>), grid, dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+
 template <int BO, int BT, int P>
 hipError_t f8_any_go(F8Args a, bool e8, hipStream_t s) {
     a.tiles_m = (int)cdiv(a.m, BO);
-    // an expert's last tile may be partial: one more tile for each that has rows, at most
-    a.tiles_t = (int)(a.offsets ? a.T / BT + (a.T < a.experts ? a.T : a.experts) : cdiv(a.T, BT));
+    a.tiles_t = (int)f8_tiles_most(a.T, a.experts, BT);
     const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
     if (e8) hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, true>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, false>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
+hipError_t f8_run(F8Args a, bool e8, bool exact, const F8Plan& p, hipStream_t s) {
+    a.splits = p.splits;
+    a.kper = p.kper;
+    hipError_t e;
+    switch (p.kind) {
+        case 0: e = f8_tile_go<256, 256, 2, 2, 1, false>(a, e8, s); break;
+        case 1: e = f8_tile_go<256, 128, 3, 4, 1, false>(a, e8, s); break;
+        case 2: e = exact ? f8_tile_go<128, 128, 4, 2, 1, true>(a, e8, s) : f8_tile_go<128, 128, 4, 2, 1, false>(a, e8, s); break;
+        case 3: e = exact ? f8_tile_go<128, 64, 4, 4, 1, true>(a, e8, s) : f8_tile_go<128, 64, 4, 4, 1, false>(a, e8, s); break;
+        case 4: e = exact ? f8_tile_go<64, 64, 4, 2, 2, true>(a, e8, s) : f8_tile_go<64, 64, 4, 2, 2, false>(a, e8, s); break;
+        case F8_ROW1: e = f8_row_go<1>(a, e8, s); break;
+        case F8_ROW2: e = f8_row_go<2>(a, e8, s); break;
+        default: e = f8_any_go<64, 64, 2>(a, e8, s); break;
+    }
+    if (e != hipSuccess || a.splits == 1) return e;
+    const dim3 grid((unsigned)cdiv(a.m, 1024), (unsigned)(a.T < 32768 ? a.T : 32768));
+    hipLaunchKernelGGL(f8_join_kernel, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-bool f8_size_ok(int64_t T, int64_t m, int64_t experts) {
-    // work-items of a launch are counted in 32 bits: 512 for each tile of 64 x 16 at least
-    return (cdiv(T, 64) + (T < experts ? T : experts)) * cdiv(m, 64) < ((int64_t)1 << 23);
-}
-size_t f8_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts) {
-    (void)T; (void)n; (void)m; (void)experts;
-    return 0;
-}
+bool f8_size_ok(int64_t T, int64_t m, int64_t experts) { return f8_plan_size_ok(T, m, experts); }
+size_t f8_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts) { return f8_plan_ws_bytes(T, n, m, experts); }
 
 hipError_t f8_launch(const F8Call& c, hipStream_t s) {
     F8Args a{};
     a.X = c.X; a.sx = c.sx; a.C = c.C; a.sw = c.sw; a.offsets = c.offsets; a.rows = c.rows; a.Y = c.Y;
     a.part = (float*)c.ws; a.ldx = c.ldx; a.ldsx = c.ldsx; a.ldy = c.ldy; a.T = c.T; a.n = c.n; a.m = c.m;
     a.xrows = c.xrows; a.experts = (int)c.experts; a.groups = (int)cdiv(c.n, F8_B); a.y_dtype = c.y_dtype;
-    a.splits = 1;
-    a.kper = c.n;
-    return f8_any_go<64, 64, 2>(a, c.e8, s);
+    // 32-bit offsets: from a tile's first row, or from X's with rows
+    const bool near = c.n < ((int64_t)1 << 24) && (c.rows ? c.xrows * c.ldx < ((int64_t)1 << 32) : c.ldx < ((int64_t)1 << 24));
+    const bool fast = c.n % 16 == 0 && c.ldx % 16 == 0 && aligned(c.X, 16) && aligned(c.C, 16) && near;
+    const bool exact = c.y_dtype == 0;
+    return f8_run(a, c.e8, exact, f8_plan(F8Shape{c.T, c.n, c.m, c.experts, exact, fast}), s);
 }
 
 }  // namespace pwq

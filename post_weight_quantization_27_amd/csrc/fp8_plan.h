@@ -1,0 +1,129 @@
+// Which kernel and how many splits of k a product of e4m3 codes takes (fp8_mm.hip): host code, no HIP,
+// so that it can be compiled and checked alone.
+#pragma once
+
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace pwq {
+
+inline int64_t f8_cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t F8_STEP = 128;           // k of a block, and of a kernel's step
+constexpr int64_t F8_SPLIT_MIN_K = 512;    // least k of a split
+
+struct F8Plan {
+    int kind;                      // F8_ROW, an index into f8_tiles, or F8_ANY
+    int splits;
+    int64_t kper;
+};
+constexpr int F8_ROW1 = -1, F8_ROW2 = -2, F8_ANY = 8;
+
+// What decides: rows of Y, d_in, d_out, experts (1: one matrix), whether the float16 instructions are
+// asked for (float32 outputs), whether operand rows start at multiples of 16 bytes and lie within
+// 32-bit offsets of a tile's base
+struct F8Shape {
+    int64_t T, n, m, experts;
+    bool exact, fast;
+};
+
+inline F8Plan f8_split(int kind, int64_t n, int64_t s) {
+    const int64_t kper = f8_cdiv(f8_cdiv(n, s < 1 ? 1 : s), F8_STEP) * F8_STEP;
+    return F8Plan{kind, (int)f8_cdiv(n, kper), kper};
+}
+
+// Tiles of bt rows: no more than these hold rows, whatever the experts' shares
+inline int64_t f8_tiles_most(int64_t T, int64_t experts, int64_t bt) {
+    if (experts <= 1) return f8_cdiv(T, bt);
+    return T / bt + (T < experts ? T : experts);
+}
+
+// What is expected of the experts' shares, which the host does not know: rows that choose any of them alike
+struct F8Shares {
+    double active, rows;           // experts that have rows, and how many each
+};
+inline F8Shares f8_shares(int64_t T, int64_t experts) {
+    if (experts <= 1) return F8Shares{1.0, (double)T};
+    const double a = (double)experts * -expm1((double)T * log1p(-1.0 / (double)experts));
+    return F8Shares{a, (double)T / a};
+}
+// tiles of bt rows: one for each expert while its rows are few, or half of its last one empty
+inline double f8_tiles_about(const F8Shares& e, int64_t T, int64_t experts, int64_t bt, double few) {
+    if (experts <= 1) return (double)f8_cdiv(T, bt);
+    return e.rows <= few ? e.active : (double)T / bt + 0.5 * e.active;
+}
+
+// What a tile costs on this chip: every compute unit holds one workgroup, which takes `fixed`
+// microseconds and `step` more for each 128 k.
+struct F8TileCost {
+    int bo, bt;
+    float fixed, step, step_exact; // us
+};
+constexpr F8TileCost f8_tiles[] = {
+    {256, 256, 10.5f, 1.27f, 0.f},         // no float16 form: its fragments do not fit the registers
+    {256, 128, 7.7f, 0.895f, 0.f},
+    {128, 128, 6.5f, 0.541f, 0.951f},
+    {128, 64, 5.75f, 0.394f, 0.627f},
+    {64, 64, 5.4f, 0.229f, 0.348f},
+};
+constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
+
+// The least estimate (us) of: rounds of tiles on 256 compute units over 1 to 8 splits of k whose sums
+// a second launch joins, and no less than memory takes; or the row kernel, whose workgroups stream their 16
+// rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359
+// shapes (768 .. 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts, each output
+// and scale type): the choice takes 2.2 % longer than the fastest kernel in the geometric mean and 41 % at
+// the worst (64 rows of 128 experts by 1024 x 2048: 36 against 26 us); 128 x 128 tiles alone take 66 % longer in
+// the mean.
+inline F8Plan f8_plan(const F8Shape& s) {
+    if (!s.fast) return F8Plan{F8_ANY, 1, s.n};
+    const F8Shares e = f8_shares(s.T, s.experts);
+    const double bytes = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6;      // MB
+    const double mem = bytes / 4.95 + 3.3;
+    F8Plan best{F8_ANY, 1, s.n};
+    double least = 1e30;
+    for (int i = 0; i < F8_TILES; ++i) {
+        const F8TileCost& c = f8_tiles[i];
+        const float step = s.exact ? c.step_exact : c.step;
+        if (step == 0.f) continue;
+        const double tiles = f8_tiles_about(e, s.T, s.experts, c.bt, c.bt / 2) * (double)f8_cdiv(s.m, c.bo);
+        for (int64_t sp = 1; sp <= 8; sp *= 2) {
+            if (sp > 1 && (s.n / sp < F8_SPLIT_MIN_K || tiles * sp > 1024.0)) break;
+            const F8Plan p = f8_split(i, s.n, sp);
+            if (sp > 1 && p.splits < sp) continue;
+            const double groups = tiles * p.splits / 256.0;
+            const double rounds = s.experts > 1 ? (groups > 0.7 ? groups + 0.3 : 1.0) : ceil(groups);
+            const double work = 0.4 + rounds * (c.fixed + step * (double)p.kper / 128.0);
+            double t = work > mem ? work + 0.05 * mem : mem + 0.05 * work;
+            if (p.splits > 1) t += 3.2 + 0.34 * (double)p.splits * s.T * s.m * 4e-6;
+            if (t < least) { least = t; best = p; }
+        }
+    }
+    if (e.rows <= 256.0 && f8_tiles_most(s.T, s.experts, 16) <= 65535) {
+        const double groups = (double)f8_cdiv(s.m, 16) * f8_tiles_about(e, s.T, s.experts, 16, 8.0) / 256.0;
+        const double one = 1e-3 * (double)s.n * (1.0 + 0.38 * (e.rows < 16.0 ? e.rows : 16.0) / 16.0) * (groups > 1.0 ? groups : 1.0);
+        const double t1 = 3.4 + 0.85 * one + 0.058 * (double)f8_cdiv(s.n, 1024);
+        const double t2 = 3.4 + 0.884 * one + 0.014 * (double)f8_cdiv(s.n, 2048);
+        if (t1 < least) { least = t1; best = f8_split(F8_ROW1, s.n, 1); }
+        if (t2 < least) best = f8_split(F8_ROW2, s.n, 1);
+    }
+    return best;
+}
+
+inline bool f8_plan_size_ok(int64_t T, int64_t m, int64_t experts) {
+    // work-items of a launch are counted in 32 bits: 512 for tiles of 64 x 64 at least
+    return f8_tiles_most(T, experts, 64) * f8_cdiv(m, 64) < ((int64_t)1 << 23) && f8_cdiv(m, 16) < ((int64_t)1 << 23);
+}
+
+inline size_t f8_plan_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts) {
+    // the outputs' type, and where rows start, are the call's affair: room for any of its plans
+    int most = 1;
+    for (int i = 0; i < (n % 16 == 0 ? 4 : 2); ++i) {
+        const F8Plan p = f8_plan(F8Shape{T, n, m, experts, (i & 1) != 0, (i & 2) != 0});
+        most = p.splits > most ? p.splits : most;
+    }
+    return most > 1 ? (size_t)most * (size_t)T * (size_t)m * sizeof(float) : 0;
+}
+
+}  // namespace pwq
