@@ -267,7 +267,7 @@ __device__ __forceinline__ uint4 f8_short(const uint8_t* row, int64_t k, int64_t
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int BO, int BT, int P, bool E8>
+template <int BO, int BT, int P, bool E8, bool EXACT>
 __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
     constexpr int BK = F8_B, FO = BO / 32, FT = BT / 32;      // fragments of a wave
     constexpr int NC = (BO + BT) / 32;                        // chunks per thread
@@ -327,24 +327,27 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
     for (int i = 0; i < FO; ++i)
 #pragma unroll
         for (int j = 0; j < FT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    auto read = [&](const uint8_t* S, int row) {              // this lane's chunks c and c + 4 of row + r
+        const uint8_t* q = S + (row + r) * BK;
+        const i32x4 u = *(const i32x4*)(q + 16 * f8_pos(r, c)), v = *(const i32x4*)(q + 16 * f8_pos(r, 4 + c));
+        return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
     auto multiply = [&](const uint8_t* S, const float (&sx)[FT], float sw) {
         f8_wait_lds();
         f8_barrier();
         f32x4 p[FO][FT];
+        i32x8 fo[FO], ft[FT];
+#pragma unroll
+        for (int i = 0; i < FO; ++i) fo[i] = read(S, wo * (BO / 2) + 16 * i);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) ft[j] = read(S, BO + wt * (BT / 2) + 16 * j);
 #pragma unroll
         for (int i = 0; i < FO; ++i)
 #pragma unroll
             for (int j = 0; j < FT; ++j) p[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if constexpr (EXACT) {
 #pragma unroll
-        for (int ks = 0; ks < BK / 64; ++ks) {
-            const int o = r * BK + 16 * f8_pos(r, 4 * ks + c);
-            i32x4 fo[FO], ft[FT];
-#pragma unroll
-            for (int i = 0; i < FO; ++i) fo[i] = *(const i32x4*)(S + (wo * (BO / 2) + 16 * i) * BK + o);
-#pragma unroll
-            for (int j = 0; j < FT; ++j) ft[j] = *(const i32x4*)(S + (BO + wt * (BT / 2) + 16 * j) * BK + o);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 4; ++h) {
                 f16x8 ho[FO], ht[FT];
 #pragma unroll
                 for (int i = 0; i < FO; ++i) ho[i] = f8_half(fo[i][2 * h], fo[i][2 * h + 1]);
@@ -355,6 +358,12 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
 #pragma unroll
                     for (int j = 0; j < FT; ++j) p[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ho[i], ht[j], p[i][j], 0, 0, 0);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < FO; ++i)
+#pragma unroll
+                for (int j = 0; j < FT; ++j)
+                    p[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fo[i], ft[j], p[i][j], 0, 0, 0, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
@@ -914,14 +923,14 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
 
 // ------------------------------------------------------------------ few tokens
 // Few tokens, where the weights are the traffic or a launch's latency counts: a workgroup owns 16
-// outputs by 16 tokens, its eight waves share k in turns of U blocks each, every lane loads its
+// outputs by 16 tokens, its W waves share k in turns of U blocks each, every lane loads its
 // fragments (16 bytes of one row) straight into registers, those of a turn while the turn before is
 // multiplied, and the waves' sums meet in LDS.  No staging: a code is used once, and X comes from L2.
 // The float16 instructions cost nothing here.  Loads past the rows or tokens take a 16-byte block of
 // zeros as their address, so none waits behind a branch.
-template <int U, bool E8>
-__global__ __launch_bounds__(512) void f8_row_kernel(F8Args a) {
-    __shared__ f32x4 red[8][64];
+template <int U, int W, bool E8>
+__global__ __launch_bounds__(64 * W) void f8_row_kernel(F8Args a) {
+    __shared__ f32x4 red[W][64];
     const F8Rows at = f8_rows<16>(a, blockIdx.z);
     if (at.t0 >= at.end) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -972,7 +981,7 @@ __global__ __launch_bounds__(512) void f8_row_kernel(F8Args a) {
         }
     };
     // turns of the whole workgroup, from a different one on each (see the tiles' order of k)
-    constexpr int TURN = 8 * U;
+    constexpr int TURN = W * U;
     const int turns = (a.groups + TURN - 1) / TURN;
     int turn = (int)(blockIdx.x % (unsigned)turns);
     auto next = [&] {
@@ -999,7 +1008,7 @@ __global__ __launch_bounds__(512) void f8_row_kernel(F8Args a) {
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) acc += red[w][lane];
+    for (int w = 1; w < W; ++w) acc += red[w][lane];
     f8_out4(a, acc, t, at.end, o0 + 4 * c, bad);
 }
 
@@ -1045,21 +1054,21 @@ hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int U>
+template <int U, int W>
 hipError_t f8_row_go(const F8Args& a, bool e8, hipStream_t s) {
     const dim3 grid((unsigned)cdiv(a.m, 16), 1, (unsigned)f8_tiles_most(a.T, a.experts, 16));
-    if (e8) hipLaunchKernelGGL((f8_row_kernel<U, true>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((f8_row_kernel<U, false>), grid, dim3(512), 0, s, a);
+    if (e8) hipLaunchKernelGGL((f8_row_kernel<U, W, true>), grid, dim3(64 * W), 0, s, a);
+    else hipLaunchKernelGGL((f8_row_kernel<U, W, false>), grid, dim3(64 * W), 0, s, a);
     return hipGetLastError();
 }
 
-template <int BO, int BT, int P>
+template <int BO, int BT, int P, bool EXACT>
 hipError_t f8_any_go(F8Args a, bool e8, hipStream_t s) {
     a.tiles_m = (int)cdiv(a.m, BO);
     a.tiles_t = (int)f8_tiles_most(a.T, a.experts, BT);
     const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
-    if (e8) hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, false>), grid, dim3(256), 0, s, a);
+    if (e8) hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, true, EXACT>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((f8_any_kernel<BO, BT, P, false, EXACT>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1073,9 +1082,11 @@ hipError_t f8_run(F8Args a, bool e8, bool exact, const F8Plan& p, hipStream_t s)
         case 2: e = exact ? f8_tile_go<128, 128, 4, 2, 1, true>(a, e8, s) : f8_tile_go<128, 128, 4, 2, 1, false>(a, e8, s); break;
         case 3: e = exact ? f8_tile_go<128, 64, 4, 4, 1, true>(a, e8, s) : f8_tile_go<128, 64, 4, 4, 1, false>(a, e8, s); break;
         case 4: e = exact ? f8_tile_go<64, 64, 4, 2, 2, true>(a, e8, s) : f8_tile_go<64, 64, 4, 2, 2, false>(a, e8, s); break;
-        case F8_ROW1: e = f8_row_go<1>(a, e8, s); break;
-        case F8_ROW2: e = f8_row_go<2>(a, e8, s); break;
-        default: e = f8_any_go<64, 64, 2>(a, e8, s); break;
+        case F8_ROW1: e = f8_row_go<2, 2>(a, e8, s); break;
+        case F8_ROW2: e = f8_row_go<4, 4>(a, e8, s); break;
+        case F8_ANY: e = exact ? f8_any_go<64, 32, 2, true>(a, e8, s) : f8_any_go<64, 32, 2, false>(a, e8, s); break;
+        case F8_ANY + 1: e = exact ? f8_any_go<64, 64, 3, true>(a, e8, s) : f8_any_go<64, 64, 3, false>(a, e8, s); break;
+        default: e = exact ? f8_any_go<128, 64, 3, true>(a, e8, s) : f8_any_go<128, 64, 3, false>(a, e8, s); break;
     }
     if (e != hipSuccess || a.splits == 1) return e;
     const dim3 grid((unsigned)cdiv(a.m, 1024), (unsigned)(a.T < 32768 ? a.T : 32768));

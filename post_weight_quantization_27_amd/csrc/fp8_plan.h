@@ -14,7 +14,7 @@ constexpr int64_t F8_STEP = 128;           // k of a block, and of a kernel's st
 constexpr int64_t F8_SPLIT_MIN_K = 512;    // least k of a split
 
 struct F8Plan {
-    int kind;                      // F8_ROW, an index into f8_tiles, or F8_ANY
+    int kind;                      // one of the below, an index into f8_tiles, or F8_ANY + one into f8_any
     int splits;
     int64_t kper;
 };
@@ -54,6 +54,45 @@ inline double f8_tiles_about(const F8Shares& e, int64_t T, int64_t experts, int6
     return e.rows <= few ? e.active : (double)T / bt + 0.5 * e.active;
 }
 
+// Any alignment: the tile and the splits of k with the least estimate (us), rounds of tiles on 256
+// compute units, of which workgroups that share one overlap a part.  Fitted to the times over 210 shapes
+// with odd d_in (517 .. 14337 inputs, 769 .. 14337 outputs, 1 .. 3000 rows, one matrix and 7 or 32
+// experts, float32 and 16-bit outputs): 1.2 % longer than the fastest in the geometric mean and 24 % at the
+// worst; 64 x 64 tiles alone, unsplit, take 31 % longer in the mean.  333 rows by 5003 x 1601, float32
+// outputs: 19.7 us with 128 x 64, 22.8 with 64 x 64, 23.3 with 64 x 32; 16 by 4099 x 8191, bfloat16: 66, 45 and 30.
+struct F8AnyCost {
+    int bo, bt;
+    float fixed, step, step_exact; // us per tile, and for each 128 k
+};
+constexpr F8AnyCost f8_any[] = {
+    {64, 32, 0.3f, 0.323f, 0.362f},
+    {64, 64, 1.07f, 0.473f, 0.585f},
+    {128, 64, 2.26f, 0.755f, 0.989f},
+};
+inline F8Plan f8_plan_any(const F8Shape& s) {
+    const F8Shares e = f8_shares(s.T, s.experts);
+    const double mem = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6 / 2.33;
+    F8Plan best{F8_ANY, 1, s.n};
+    double least = 1e30;
+    for (int i = 0; i < (int)(sizeof(f8_any) / sizeof(f8_any[0])); ++i) {
+        const F8AnyCost& c = f8_any[i];
+        const double tiles = f8_tiles_about(e, s.T, s.experts, c.bt, c.bt / 2) * (double)f8_cdiv(s.m, c.bo);
+        for (int64_t sp = 1; sp <= 8; sp *= 2) {
+            if (sp > 1 && (s.n / sp < F8_SPLIT_MIN_K || tiles * sp > 2000.0)) break;
+            const F8Plan p = f8_split(F8_ANY + i, s.n, sp);
+            if (sp > 1 && p.splits < sp) continue;
+            const double groups = tiles * p.splits / 256.0;
+            const double rounds = s.experts > 1 ? (groups > 0.7 ? groups + 0.3 : 1.0) : ceil(groups);
+            const double load = 0.175 * (groups > 1.0 ? groups : 1.0) + 0.825 * rounds;
+            const double work = 4.2 + load * (c.fixed + (s.exact ? c.step_exact : c.step) * (double)f8_cdiv(p.kper, 128));
+            double t = work > mem ? work + 0.05 * mem : mem + 0.05 * work;
+            if (p.splits > 1) t += 3.4 + 0.28 * (double)p.splits * s.T * s.m * 4e-6;
+            if (t < least) { least = t; best = p; }
+        }
+    }
+    return best;
+}
+
 // What a tile costs on this chip: every compute unit holds one workgroup, which takes `fixed`
 // microseconds and `step` more for each 128 k.
 struct F8TileCost {
@@ -61,11 +100,11 @@ struct F8TileCost {
     float fixed, step, step_exact; // us
 };
 constexpr F8TileCost f8_tiles[] = {
-    {256, 256, 10.5f, 1.27f, 0.f},         // no float16 form: its fragments do not fit the registers
-    {256, 128, 7.7f, 0.895f, 0.f},
-    {128, 128, 6.5f, 0.541f, 0.951f},
-    {128, 64, 5.75f, 0.394f, 0.627f},
-    {64, 64, 5.4f, 0.229f, 0.348f},
+    {256, 256, 9.2f, 1.29f, 0.f},          // no float16 form: its fragments do not fit the registers
+    {256, 128, 7.3f, 0.88f, 0.f},
+    {128, 128, 6.25f, 0.527f, 0.945f},
+    {128, 64, 5.65f, 0.385f, 0.624f},
+    {64, 64, 5.2f, 0.227f, 0.345f},
 };
 constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 
@@ -73,14 +112,14 @@ constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 // a second launch joins, and no less than memory takes; or the row kernel, whose workgroups stream their 16
 // rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359
 // shapes (768 .. 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts, each output
-// and scale type): the choice takes 2.2 % longer than the fastest kernel in the geometric mean and 41 % at
-// the worst (64 rows of 128 experts by 1024 x 2048: 36 against 26 us); 128 x 128 tiles alone take 66 % longer in
-// the mean.
+// and scale type): the choice takes 2.0 % longer than the fastest kernel in the geometric mean and 32 % at
+// the worst (192 rows by 768 x 768: 7.3 against 5.5 us); 128 x 128 tiles alone take 58 % longer in the
+// mean and up to 5.8 times as long.
 inline F8Plan f8_plan(const F8Shape& s) {
-    if (!s.fast) return F8Plan{F8_ANY, 1, s.n};
+    if (!s.fast) return f8_plan_any(s);
     const F8Shares e = f8_shares(s.T, s.experts);
     const double bytes = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6;      // MB
-    const double mem = bytes / 4.95 + 3.3;
+    const double mem = bytes / 5.0 + 2.7;
     F8Plan best{F8_ANY, 1, s.n};
     double least = 1e30;
     for (int i = 0; i < F8_TILES; ++i) {
@@ -94,17 +133,17 @@ inline F8Plan f8_plan(const F8Shape& s) {
             if (sp > 1 && p.splits < sp) continue;
             const double groups = tiles * p.splits / 256.0;
             const double rounds = s.experts > 1 ? (groups > 0.7 ? groups + 0.3 : 1.0) : ceil(groups);
-            const double work = 0.4 + rounds * (c.fixed + step * (double)p.kper / 128.0);
+            const double work = 0.7 + rounds * (c.fixed + step * (double)p.kper / 128.0);
             double t = work > mem ? work + 0.05 * mem : mem + 0.05 * work;
-            if (p.splits > 1) t += 3.2 + 0.34 * (double)p.splits * s.T * s.m * 4e-6;
+            if (p.splits > 1) t += 3.4 + 0.31 * (double)p.splits * s.T * s.m * 4e-6;
             if (t < least) { least = t; best = p; }
         }
     }
     if (e.rows <= 256.0 && f8_tiles_most(s.T, s.experts, 16) <= 65535) {
         const double groups = (double)f8_cdiv(s.m, 16) * f8_tiles_about(e, s.T, s.experts, 16, 8.0) / 256.0;
-        const double one = 1e-3 * (double)s.n * (1.0 + 0.38 * (e.rows < 16.0 ? e.rows : 16.0) / 16.0) * (groups > 1.0 ? groups : 1.0);
-        const double t1 = 3.4 + 0.85 * one + 0.058 * (double)f8_cdiv(s.n, 1024);
-        const double t2 = 3.4 + 0.884 * one + 0.014 * (double)f8_cdiv(s.n, 2048);
+        const double one = 1e-3 * (double)s.n * (1.0 + 0.335 * (e.rows < 16.0 ? e.rows : 16.0) / 16.0) * (groups > 1.0 ? groups : 1.0);
+        const double t1 = 3.2 + 0.74 * one + 0.695 * (double)f8_cdiv(s.n, 1024);
+        const double t2 = 3.2 + 0.909 * one + 0.255 * (double)f8_cdiv(s.n, 2048);
         if (t1 < least) { least = t1; best = f8_split(F8_ROW1, s.n, 1); }
         if (t2 < least) best = f8_split(F8_ROW2, s.n, 1);
     }

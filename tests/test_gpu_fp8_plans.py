@@ -18,6 +18,11 @@ PRODUCTS = [  # rows, d_in, d_out, experts
     (1, 48, 40, 6), (1030, 400, 136, 6), (1300, 1040, 6152, 6), (65, 1040, 8200, 6), (1600, 48, 2056, 6), (2060, 1040, 776, 6),
     (520, 1040, 3100, 6), (2060, 48, 776, 6), (100, 1040, 3100, 6), (130, 1040, 3100, 6), (1600, 1040, 40, 6), (40, 8208, 40, 6),
     (65, 8208, 40, 6), (100, 6160, 776, 6), (130, 8208, 776, 6), (2060, 8208, 72, 6), (1030, 8208, 200, 6),
+    (65, 400, 4104, 1), (65, 8208, 2056, 1), (400, 48, 6152, 6), (24, 1040, 8200, 6), (400, 48, 2696, 1), (1, 12304, 2056, 1), (700, 1040, 2056, 6),
+    # rows that start at any byte
+    (1, 45, 40, 1), (1, 2065, 40, 1), (100, 1041, 8200, 1), (130, 401, 4104, 1), (257, 1041, 1800, 1), (257, 1041, 5512, 1),
+    (700, 149, 5512, 1), (1030, 4113, 72, 1), (1600, 8209, 72, 1), (1600, 8209, 136, 1), (40, 8209, 6152, 1), (1, 1041, 40, 6),
+    (700, 1041, 2056, 6), (1030, 1041, 2056, 6), (1600, 1041, 520, 6), (1600, 2065, 520, 6), (1600, 4113, 72, 6), (1600, 401, 5512, 6),
 ]
 
 
