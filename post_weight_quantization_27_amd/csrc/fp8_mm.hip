@@ -54,44 +54,56 @@ struct F8Rows {
     int expert;
 };
 
-// Tile tt of BT rows: the experts' rows are cut into tiles one expert after the other.  Every wave
-// counts through the offsets, 64 experts at a time.  Offsets are taken into 0 .. T, so whatever they
-// hold no row outside Y is touched.
+// The experts' rows are cut into tiles of BT, one expert after the other.  Every wave counts them through
+// the offsets, 64 experts at a time.  Offsets are taken into 0 .. T, so whatever they hold no row outside Y
+// is touched.
 template <int BT>
-__device__ __forceinline__ F8Rows f8_rows(const F8Args& a, int tt) {
-    if (!a.offsets) return F8Rows{(int64_t)tt * BT, a.T, 0};
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 64) {
-        int64_t lo = 0, hi = 0;
+struct F8Count {
+    int64_t lo, hi;                // of this lane's expert
+    int own, upto;                 // its tiles, and those of the experts up to it (of the same 64)
+    __device__ __forceinline__ int of(const F8Args& a, int e0) {      // tiles of the 64 experts from e0 on
+        const int lane = threadIdx.x & 63;
+        lo = hi = 0;
         if (e0 + lane < a.experts) {
             lo = a.offsets[e0 + lane];
             hi = a.offsets[e0 + lane + 1];
             lo = lo < 0 ? 0 : lo;
             hi = hi > a.T ? a.T : hi;
         }
-        const int own = hi > lo ? (int)((hi - lo + BT - 1) / BT) : 0;
-        int sum = own;                                    // tiles of the experts up to this one
+        own = hi > lo ? (int)((hi - lo + BT - 1) / BT) : 0;
+        upto = own;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(sum, o, 64);
-            if (lane >= o) sum += v;
+            const int v = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += v;
         }
-        const uint64_t past = __ballot(before + sum > tt);
-        if (past) {
-            const int src = __builtin_ctzll(past);
-            const int64_t t0 = lo + (int64_t)(tt - before - (sum - own)) * BT;
-            F8Rows r;
-            r.t0 = ((int64_t)__builtin_amdgcn_readlane((int)(t0 >> 32), src) << 32) |
-                   (uint32_t)__builtin_amdgcn_readlane((int)t0, src);
-            r.end = ((int64_t)__builtin_amdgcn_readlane((int)(hi >> 32), src) << 32) |
-                    (uint32_t)__builtin_amdgcn_readlane((int)hi, src);
-            r.expert = e0 + src;
-            return r;
-        }
-        before += __builtin_amdgcn_readlane(sum, 63);
+        return __builtin_amdgcn_readlane(upto, 63);
     }
-    return F8Rows{0, 0, 0};
+    // the rows of tile tt of these 64 experts, if it is one of theirs
+    __device__ __forceinline__ bool find(int e0, int tt, F8Rows& r) const {
+        const uint64_t past = __ballot(upto > tt);
+        if (!past) return false;
+        const int src = __builtin_ctzll(past);
+        const int64_t t0 = lo + (int64_t)(tt - (upto - own)) * BT;
+        r.t0 = ((int64_t)__builtin_amdgcn_readlane((int)(t0 >> 32), src) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)t0, src);
+        r.end = ((int64_t)__builtin_amdgcn_readlane((int)(hi >> 32), src) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)hi, src);
+        r.expert = e0 + src;
+        return true;
+    }
+};
+
+// Tile tt of BT rows
+template <int BT>
+__device__ __forceinline__ F8Rows f8_rows(const F8Args& a, int tt) {
+    if (!a.offsets) return F8Rows{(int64_t)tt * BT, a.T, 0};
+    F8Rows r{0, 0, 0};
+    F8Count<BT> c;
+    for (int e0 = 0; e0 < a.experts; e0 += 64) {
+        const int n = c.of(a, e0);
+        if (c.find(e0, tt, r)) break;
+        tt -= n;
+    }
+    return r;
 }
 
 // X's row for output row t; bad indexes read row 0 and give NaN (f8_bad)
@@ -104,17 +116,30 @@ __device__ __forceinline__ bool f8_bad(const F8Args& a, int64_t t) {
     return a.rows && (uint32_t)a.rows[t] >= (uint64_t)a.xrows;
 }
 
-// bid -> tile: consecutive workgroups go to different XCDs, so each XCD takes a contiguous share
-// of the tiles, in groups of up to 8 output tiles by all token tiles
-__device__ __forceinline__ void f8_map(const F8Args& a, int64_t bid, int& to, int& tt) {
-    const int64_t nt = (int64_t)a.tiles_t * a.tiles_m;
+// bid -> tile of BT rows by outputs: consecutive workgroups go to different XCDs, so each XCD takes a
+// contiguous share of the tiles, in groups of up to 8 output tiles by all token tiles.  With experts the
+// shares are of the tiles that hold rows: of those that might, which are launched, the last ones hold none
+// (32768 rows of 64 experts by 4096 x 4096: 708 us with shares of all).
+template <int BT>
+__device__ __forceinline__ bool f8_tile(const F8Args& a, int64_t bid, int& to, F8Rows& r) {
+    F8Count<BT> c;
+    int64_t tiles_t = a.tiles_t;
+    if (a.offsets) {
+        tiles_t = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) tiles_t += c.of(a, e0);
+    }
+    const int64_t nt = tiles_t * a.tiles_m;
+    if (bid >= nt) return false;
     const int64_t x = bid & 7, per = nt >> 3, rem = nt & 7;
     const int64_t id = x * per + (x < rem ? x : rem) + (bid >> 3);
-    const int64_t band = 8 * (int64_t)a.tiles_t, g = id / band;
+    const int64_t band = 8 * tiles_t, g = id / band;
     const int rows = a.tiles_m - 8 * g < 8 ? (int)(a.tiles_m - 8 * g) : 8;
     const int in = (int)(id - g * band);
-    tt = in / rows;
+    const int tt = in / rows;
     to = (int)(8 * g) + in - tt * rows;
+    if (a.offsets && a.experts <= 64) return c.find(0, tt, r);
+    r = f8_rows<BT>(a, tt);
+    return r.t0 < r.end;
 }
 
 // ------------------------------------------------------------------ scales
@@ -274,10 +299,9 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
     constexpr int ST = (BO + BT) * BK;
     static_assert(BO <= 256, "a wave's outputs share a block");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * ST];
-    int to, tt;
-    f8_map(a, blockIdx.x, to, tt);
-    const F8Rows at_rows = f8_rows<BT>(a, tt);
-    if (at_rows.t0 >= at_rows.end) return;
+    int to;
+    F8Rows at_rows{0, 0, 0};
+    if (!f8_tile<BT>(a, blockIdx.x, to, at_rows)) return;
     const int64_t o0 = (int64_t)to * BO, t0 = at_rows.t0, tend = at_rows.end;
     const int64_t kbeg = (int64_t)blockIdx.y * a.kper;
     const int64_t kend = kbeg + a.kper < a.n ? kbeg + a.kper : a.n;
@@ -517,10 +541,8 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     constexpr int ROT = BT <= 128 ? 3 : 0;
     int rot;
     auto setup = [&](int64_t tile) {
-        int to, tt;
-        f8_map(a, tile, to, tt);
-        at = f8_rows<BT>(a, tt);
-        if (at.t0 >= at.end) return false;
+        int to;
+        if (!f8_tile<BT>(a, tile, to, at)) return false;
         o0 = (int64_t)to * BO;
         rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
         cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
@@ -730,18 +752,15 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     const int64_t tiles = (int64_t)a.tiles_t * a.tiles_m;
     int64_t tile = blockIdx.x;
     auto next = [&] {                                     // the first stages of the next tile that has rows
-        for (; tile < tiles; tile += gridDim.x) {
-            if (!setup(tile)) continue;
-            if constexpr (TWO) {
-                copy_some(0, 0, L + 1);
-                copy_some(1, 0, grp == 0 ? 5 : L + 1);
-            } else {
-                for (int q = 0; q < NST - 1; ++q) copy_some(q, 0, L + 1);
-                if (INSIDE && (KG == 2 || grp == 1)) copy_some(NST - 1, 0, L + 1);
-            }
-            return true;
+        if (tile >= tiles || !setup(tile)) return false;
+        if constexpr (TWO) {
+            copy_some(0, 0, L + 1);
+            copy_some(1, 0, grp == 0 ? 5 : L + 1);
+        } else {
+            for (int q = 0; q < NST - 1; ++q) copy_some(q, 0, L + 1);
+            if (INSIDE && (KG == 2 || grp == 1)) copy_some(NST - 1, 0, L + 1);
         }
-        return false;
+        return true;
     };
     if (!next()) return;
     for (;;) {
