@@ -485,6 +485,7 @@ def quantized_matmul_noalloc(X: torch.Tensor, packed: torch.Tensor, scales: torc
 _CODES = {torch.float32: PWQ_F32, torch.float16: PWQ_F16, torch.bfloat16: PWQ_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _bad(name: str, want: str):
@@ -518,10 +519,11 @@ def _on(X: torch.Tensor, call, *args):
     dev = X.device
     if dev.type != "cuda":
         _bad("X", "a GPU tensor")
-    if torch.cuda.current_device() == dev.index:
-        return call(*args, _raw_stream(dev.index))
+    index = dev.index
+    if _current_device() == index:
+        return call(*args, _raw_stream(index))
     with torch.cuda.device(dev):
-        return call(*args, _raw_stream(dev.index))
+        return call(*args, _raw_stream(index))
 
 
 def _token_outputs(o: dict, T: int, d: int, dev, want_sums: bool):
@@ -659,40 +661,37 @@ _E4M3 = torch.float8_e4m3fn
 _SCALES = {torch.float32: 0, torch.float8_e8m0fnu: 1}
 
 
-def _dense(t: torch.Tensor, name: str, dtypes, dev, shape) -> int:
+def _dense(t: torch.Tensor, name: str, dtype, dev, shape) -> int:
     """Address of a contiguous tensor of `shape` on dev."""
-    if t.dtype not in dtypes or t.device != dev or t.shape != shape or not t.is_contiguous():
-        _bad(name, f"contiguous {tuple(shape)} of {' / '.join(map(str, dtypes))} on {dev}")
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _bad(name, f"contiguous {tuple(shape)} of {dtype} on {dev}")
     return t.data_ptr()
-
-
-def _fp8_outputs(o: dict, codes_shape, scales_shape, scale_dtype, dev):
-    """(codes, scales) of o, made where missing."""
-    if scale_dtype not in _SCALES:
-        _bad("scale_dtype", "torch.float32 or torch.float8_e8m0fnu")
-    if o.get("codes") is None:
-        o["codes"] = torch.empty(codes_shape, dtype=_E4M3, device=dev)
-    if o.get("scales") is None:
-        o["scales"] = torch.empty(scales_shape, dtype=scale_dtype, device=dev)
-    return o["codes"], o["scales"]
 
 
 def quantize_tokens_fp8(X: torch.Tensor, scale_dtype=torch.float32, out: Optional[dict] = None) -> dict:
     """e4m3 codes of activations with a scale per token and 128 values: {codes (tokens x d,
     float8_e4m3fn), scales (d / 128 rounded up x tokens, ``scale_dtype``: float32, or float8_e8m0fnu
-    for powers of two)}.  ``out`` may hold tensors to write into."""
+    for powers of two)}.  ``out`` may hold tensors to write into (a scale tensor there says the type)."""
     dev = X.device
     if dev.type != "cuda":
         _bad("X", "a GPU tensor")
     ldx = _pitch(X, "X", _CODES, dev)
     T, d = X.shape
-    G = -(-d // 128)
+    G = (d + 127) // 128
     o = out if out is not None else {}
-    if o.get("scales") is not None:
-        scale_dtype = o["scales"].dtype
-    q, s = _fp8_outputs(o, (T, d), (G, T), scale_dtype, dev)
-    ldq = _pitch(q, "codes", (_E4M3,), dev, (T, d))
-    lds = _pitch(s, "scales", (scale_dtype,), dev, (G, T))
+    q, s, ldq, lds = o.get("codes"), o.get("scales"), d, T
+    if s is not None:
+        scale_dtype = s.dtype
+    if scale_dtype not in _SCALES:
+        _bad("scale_dtype", "torch.float32 or torch.float8_e8m0fnu")
+    if q is None:
+        q = o["codes"] = torch.empty(T, d, dtype=_E4M3, device=dev)
+    else:
+        ldq = _pitch(q, "codes", (_E4M3,), dev, (T, d))
+    if s is None:
+        s = o["scales"] = torch.empty(G, T, dtype=scale_dtype, device=dev)
+    else:
+        lds = _pitch(s, "scales", (scale_dtype,), dev, (G, T))
     _check("pwq_quantize_tokens_fp8", _on(X, lib().pwq_quantize_tokens_fp8, X.data_ptr(), _CODES[X.dtype], T, d, ldx,
                                           _SCALES[scale_dtype], q.data_ptr(), ldq, s.data_ptr(), lds))
     return o
@@ -717,58 +716,79 @@ def quantize_blocks_fp8(W: torch.Tensor, scale_dtype=torch.float32, out: Optiona
     o = out if out is not None else {}
     if o.get("scales") is not None:
         scale_dtype = o["scales"].dtype
+    if scale_dtype not in _SCALES:
+        _bad("scale_dtype", "torch.float32 or torch.float8_e8m0fnu")
     shape = (*W.shape[:-2], -(-m // 128), -(-d // 128))
-    q, s = _fp8_outputs(o, W.shape, shape, scale_dtype, dev)
-    _dense(q, "codes", (_E4M3,), dev, W.shape)
-    _dense(s, "scales", (scale_dtype,), dev, shape)
+    if o.get("codes") is None:
+        o["codes"] = torch.empty(W.shape, dtype=_E4M3, device=dev)
+    if o.get("scales") is None:
+        o["scales"] = torch.empty(shape, dtype=scale_dtype, device=dev)
+    q, s = o["codes"], o["scales"]
+    _dense(q, "codes", _E4M3, dev, W.shape)
+    _dense(s, "scales", scale_dtype, dev, shape)
     _check("pwq_quantize_blocks_fp8", _on(W, lib().pwq_quantize_blocks_fp8, W.data_ptr(), _CODES[W.dtype], E, m, d, ldw,
                                           stride, _SCALES[scale_dtype], q.data_ptr(), s.data_ptr()))
     return o
 
 
-def _fp8_x(X: torch.Tensor, x_scales: torch.Tensor, dev):
-    """(pitch of X, pitch of its scales, scale type)"""
-    if dev.type != "cuda":
-        _bad("X", "a GPU tensor")
-    ldx = _pitch(X, "X", (_E4M3,), dev)
-    T, d = X.shape
-    return ldx, _pitch(x_scales, "x_scales", _SCALES, dev, (-(-d // 128), T)), _SCALES[x_scales.dtype]
+_FP8_WS: dict = {}                  # bytes of workspace by sizes: one token's call costs less than asking
 
 
-def _fp8_ws(ws, need: int, dev):
-    """(address, bytes) of the workspace"""
+def _fp8_ws(ws: Optional[torch.Tensor], dev, *sizes):
+    """(address, bytes) of the workspace for rows, d_in, d_out and experts, made if there is none, and its tensor"""
+    need = _FP8_WS.get(sizes)
+    if need is None:
+        if len(_FP8_WS) >= 4096:
+            _FP8_WS.clear()
+        need = _FP8_WS[sizes] = lib().pwq_quantized_matmul_fp8_grouped_workspace_size(*sizes)
     if not need:
-        return None, 0
+        return None, 0, None
     if ws is None:
         ws = _ws(need, dev)
     elif ws.device != dev or not ws.is_contiguous():
         _bad("ws", f"contiguous bytes on {dev}")
-    return ws, ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _fp8_operands(X, x_scales, codes, scales, dev, rank: int):
+    """(X's pitch, its scales' pitch, scale type, addresses of codes and scales)"""
+    if dev.type != "cuda":
+        _bad("X", "a GPU tensor")
+    sh, st = codes.shape, x_scales.dtype
+    if X.dtype is not _E4M3 or not X.is_contiguous() or X.dim() != 2:
+        ldx = _pitch(X, "X", (_E4M3,), dev)
+    else:
+        ldx = X.shape[1]
+    T, d = X.shape
+    G = (d + 127) // 128
+    lds = T
+    if st not in _SCALES or x_scales.shape != (G, T) or not x_scales.is_contiguous() or x_scales.device != dev:
+        lds = _pitch(x_scales, "x_scales", _SCALES, dev, (G, T))
+    if len(sh) != rank or sh[-1] != d or codes.dtype is not _E4M3 or codes.device != dev or not codes.is_contiguous():
+        _bad("codes", f"contiguous {'d_out' if rank == 2 else 'experts x d_out'} x {d} {_E4M3} on {dev}")
+    sw = _dense(scales, "scales", st, dev, (*sh[:-2], (sh[-2] + 127) // 128, G) if rank > 2 else ((sh[0] + 127) // 128, G))
+    return ldx, lds, _SCALES[st], codes.data_ptr(), sw
 
 
 def quantized_matmul_fp8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                          out_dtype=torch.float16, out: Optional[torch.Tensor] = None,
                          ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = X What^T on e4m3 codes with a scale per block of 128: X, x_scales from quantize_tokens_fp8,
-    codes, scales from quantize_blocks_fp8 (both scales of one type)."""
+    codes, scales from quantize_blocks_fp8 (both scales of one type).  float32 outputs are sums of exact
+    products in float32; 16-bit ones may go through the e4m3 matrix instruction, whose sums are off by up to
+    2^-10 of the largest product of each eight."""
     dev = X.device
-    ldx, lds, st = _fp8_x(X, x_scales, dev)
+    ldx, lds, st, c, sw = _fp8_operands(X, x_scales, codes, scales, dev, 2)
     T, d = X.shape
-    if codes.dim() != 2:
-        _bad("codes", f"d_out x {d}")
-    m = codes.shape[0]
-    c = _dense(codes, "codes", (_E4M3,), dev, (m, d))
-    sw = _dense(scales, "scales", (x_scales.dtype,), dev, (-(-m // 128), -(-d // 128)))
-    ldy = m
+    ldy = m = codes.shape[0]
     if out is None:
         out = torch.empty(T, m, dtype=out_dtype, device=dev)
     else:
         ldy = _pitch(out, "out", _CODES, dev, (T, m))
-    L = lib()
-    ws, nb = _fp8_ws(ws, L.pwq_quantized_matmul_fp8_workspace_size(T, d, m), dev)
+    w, nb, ws = _fp8_ws(ws, dev, T, d, m, 1)
     _check("pwq_quantized_matmul_fp8", _on(
-        X, L.pwq_quantized_matmul_fp8, X.data_ptr(), T, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, out.data_ptr(),
-        _CODES.get(out.dtype, -1), ldy, ws.data_ptr() if nb else None, nb))
+        X, lib().pwq_quantized_matmul_fp8, X.data_ptr(), T, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, out.data_ptr(),
+        _CODES.get(out.dtype, -1), ldy, w, nb))
     return out
 
 
@@ -777,18 +797,14 @@ def quantized_matmul_fp8_grouped(X: torch.Tensor, x_scales: torch.Tensor, codes:
                                  out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """quantized_matmul_fp8 with one of several weight matrices for each row: codes (experts x d_out x
     d_in) and scales from quantize_blocks_fp8 of the stack.  Output rows offsets[e] .. offsets[e + 1] - 1
-    (int32 on the GPU, experts + 1 of them) multiply expert e's.  ``rows`` (int32 on the GPU): row i
-    reads row rows[i] of X, so that X need not hold a token once per expert; without it, row i of X.
-    Rows of ``out`` before the first expert's and behind the last one's are left as they are (of a new
-    tensor: whatever memory held)."""
+    (int32 on the GPU, experts + 1 of them, not decreasing) multiply expert e's.  ``rows`` (int32 on the
+    GPU): row i reads row rows[i] of X, so that X need not hold a token once per expert (an index outside X
+    gives a row of NaN); without it, row i of X.  Rows of ``out`` before the first expert's and behind the
+    last one's are left as they are (of a new tensor: whatever memory held)."""
     dev = X.device
-    ldx, lds, st = _fp8_x(X, x_scales, dev)
+    ldx, lds, st, c, sw = _fp8_operands(X, x_scales, codes, scales, dev, 3)
     n_x, d = X.shape
-    if codes.dim() != 3:
-        _bad("codes", f"experts x d_out x {d}")
     E, m = codes.shape[:2]
-    c = _dense(codes, "codes", (_E4M3,), dev, (E, m, d))
-    sw = _dense(scales, "scales", (x_scales.dtype,), dev, (E, -(-m // 128), -(-d // 128)))
     off = _vec(offsets, "offsets", (torch.int32,), dev, E + 1)
     T, r = n_x, None
     if rows is not None:
@@ -799,11 +815,10 @@ def quantized_matmul_fp8_grouped(X: torch.Tensor, x_scales: torch.Tensor, codes:
         out = torch.empty(T, m, dtype=out_dtype, device=dev)
     else:
         ldy = _pitch(out, "out", _CODES, dev, (T, m))
-    L = lib()
-    ws, nb = _fp8_ws(ws, L.pwq_quantized_matmul_fp8_grouped_workspace_size(T, d, m, E), dev)
+    w, nb, ws = _fp8_ws(ws, dev, T, d, m, E)
     _check("pwq_quantized_matmul_fp8_grouped", _on(
-        X, L.pwq_quantized_matmul_fp8_grouped, X.data_ptr(), n_x, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, E, off, r,
-        T, out.data_ptr(), _CODES.get(out.dtype, -1), ldy, ws.data_ptr() if nb else None, nb))
+        X, lib().pwq_quantized_matmul_fp8_grouped, X.data_ptr(), n_x, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, E, off,
+        r, T, out.data_ptr(), _CODES.get(out.dtype, -1), ldy, w, nb))
     return out
 
 
