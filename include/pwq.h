@@ -538,6 +538,11 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy.
  *   ws        pwq_quantized_matmul_fp8_workspace_size(n_tok, d_in, d_out) bytes, 16-byte aligned (0
  *             bytes: ws may be NULL): the float32 sums of a split k.
+ * A block's sum over k is multiplied by the product of its two scales, formed in float32, and added to a
+ * float32 sum.  With float32 Y that sum over k is of exact products in float32.  With 16-bit Y it may come
+ * from the e4m3 matrix instruction, which of each eight consecutive products keeps what is at least 2^-13
+ * of the largest: off by less than 2^-10 of the largest of each eight (about 5e-5 of the result's norm on
+ * normal data, a rounding to float16 2e-4).
  * Any alignment and sizes; rows of X and codes that start at multiples of 16 bytes take the faster
  * kernels.  Codes of NaN and scales of NaN give NaN.
  *
@@ -547,7 +552,7 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *   X         n_x x d_in; x_scales groups x n_x, leading dimension lds.  Without rows n_x = n_rows.
  *   codes     n_experts x d_out x d_in, scales n_experts x (d_out / 128) x groups, dense.
  *   offsets   DEVICE int32[n_experts + 1], not decreasing, 0 .. n_rows.  What lies outside is taken as
- *             the nearer end; of experts whose rows overlap, either may write them.
+ *             the nearer end; offsets that decrease leave Y's rows undefined.
  *   rows      optional DEVICE int32[n_rows], 0 .. n_x - 1, one row as often as wanted.  Another index
  *             gives a row of NaN.
  *   Y         n_rows x d_out; rows before offsets[0] and from offsets[n_experts] on are left alone.

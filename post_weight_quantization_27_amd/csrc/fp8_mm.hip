@@ -55,8 +55,8 @@ struct F8Rows {
 };
 
 // The experts' rows are cut into tiles of BT, one expert after the other.  Every wave counts them through
-// the offsets, 64 experts at a time.  Offsets are taken into 0 .. T, so whatever they hold no row outside Y
-// is touched.
+// the offsets, 64 experts at a time.  Offsets are taken into 0 .. T, and a tile has to start inside its
+// expert's rows, so whatever the offsets hold no row outside Y is touched.
 template <int BT>
 struct F8Count {
     int64_t lo, hi;                // of this lane's expert
@@ -84,7 +84,7 @@ struct F8Count {
         const uint64_t past = __ballot(upto > tt);
         if (!past) return false;
         const int src = __builtin_ctzll(past);
-        const int64_t t0 = lo + (int64_t)(tt - (upto - own)) * BT;
+        const int64_t t = lo + (int64_t)(tt - (upto - own)) * BT, t0 = t >= lo && t < hi ? t : hi;
         r.t0 = ((int64_t)__builtin_amdgcn_readlane((int)(t0 >> 32), src) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)t0, src);
         r.end = ((int64_t)__builtin_amdgcn_readlane((int)(hi >> 32), src) << 32) | (uint32_t)__builtin_amdgcn_readlane((int)hi, src);
         r.expert = e0 + src;
@@ -137,8 +137,8 @@ __device__ __forceinline__ bool f8_tile(const F8Args& a, int64_t bid, int& to, F
     const int in = (int)(id - g * band);
     const int tt = in / rows;
     to = (int)(8 * g) + in - tt * rows;
-    if (a.offsets && a.experts <= 64) return c.find(0, tt, r);
-    r = f8_rows<BT>(a, tt);
+    if (a.offsets && a.experts <= 64) c.find(0, tt, r);
+    else r = f8_rows<BT>(a, tt);
     return r.t0 < r.end;
 }
 
@@ -463,8 +463,15 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
 //           its own that its own waves copy; the two sums meet in LDS at the end.
 // NST stages: a stage's copies fly while the NST - 1 before it are used.  With two (256 x 256, whose
 // stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that the fragments
-// fit the registers; every wave starts the copies of stage s + 1 when the first group starts to read
-// stage s, by when the second has read stage s - 1, and waits for them a whole step later.
+// fit the registers, and each part of a stage is copied over as soon as it has been read (see the loop).
+//
+// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1460-1560 us with
+// float32 scales (2.5-2.6 PFLOP/s), 1310-1390 with powers of two (2.8-2.9), where the library's product
+// with one scale per tensor takes 1200-1330 on the same boards.  The clock falls to 1.75-2.0 GHz; a step of
+// 256 x 256 takes 2340 cycles with powers of two and about 3000 with float32 scales, of 2048 that its
+// instructions need.  One workgroup per compute unit going through its tiles loses with these (its next
+// tile's addresses spill: 8192^3 5 %, 2048 by 8192 x 8192 with powers of two 96 -> 107 us), as does leaving
+// out the instructions of waves without tokens (1460 -> 1560).
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 __device__ const uint4 f8_zeros = {0u, 0u, 0u, 0u};

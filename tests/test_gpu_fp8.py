@@ -375,6 +375,75 @@ def test_grouped_bad_indexes_and_offsets(pwq):
     assert (Y[30:] == 7).all()
 
 
+def test_grouped_offsets_in_any_order_stay_inside(pwq):
+    """Offsets that decrease: whatever the rows become, nothing outside them is written."""
+    rng = np.random.default_rng(7)
+    n, m, E, T = 256, 40, 150, 60
+    args = (e4m3(random_codes(rng, T, n)), as_scales(random_scales(rng, False, 2, T)), e4m3(random_codes(rng, E, m, n)),
+            as_scales(random_scales(rng, False, E, 1, 2)))
+    buf = torch.full((T + 2, m + 2), 7.0, dtype=torch.float32, device=DEV)
+    for off in ([0, T] * 75 + [0], [T, 0] * 75 + [T], rng.integers(-2 ** 31, 2 ** 31, E + 1), rng.integers(-5, T + 5, E + 1),
+                [2 ** 31 - 1] * (E + 1), [-2 ** 31] * (E + 1)):
+        buf.fill_(7.0)
+        pwq.quantized_matmul_fp8_grouped(*args, torch.tensor(np.asarray(off), dtype=torch.int32, device=DEV), out=buf[1:-1, 1:-1])
+        torch.cuda.synchronize()
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all() and (buf[:, 0] == 7).all() and (buf[:, -1] == 7).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_strides_up_to_32_bit_offsets(pwq, out):
+    """Rows of X so far apart that offsets from a tile's first row, or from X's, just fit 32 bits, or do not."""
+    rng = np.random.default_rng(11)
+    n, m = 1040, 264
+    C = random_codes(rng, m, n)
+    sw = random_scales(rng, False, 3, 9)
+    flat = torch.zeros((1 << 32) + (1 << 22), dtype=torch.uint8, device=DEV)
+    for T, ld in ((256, (1 << 24) - 16), (250, 1 << 24)):
+        X, sx = random_codes(rng, T, n), random_scales(rng, False, 9, T)
+        x = flat[16:16 + T * ld].view(T, ld)[:, :n]
+        x.copy_(torch.from_numpy(X).to(DEV))
+        y = pwq.quantized_matmul_fp8(x.view(torch.float8_e4m3fn), as_scales(sx), e4m3(C), as_scales(sw), out_dtype=TYPES[out])
+        check_product(y, X, sx, C, sw, TYPES[out])
+    for xrows, ld in (((1 << 18) - 1, 1 << 14), ((1 << 18) + 64, 1 << 14)):
+        x = flat[:xrows * ld].view(xrows, ld)[:, :n]
+        at = np.unique(np.concatenate([[0, xrows - 1], rng.integers(0, xrows, 200)]))
+        X = random_codes(rng, len(at), n)
+        where = torch.from_numpy(at).to(DEV)
+        x[where] = torch.from_numpy(X).to(DEV)
+        sx = np.ones((9, xrows), dtype=np.float32)
+        pick = rng.integers(0, len(at), 300)
+        off = np.array([0, 100, 300], dtype=np.int32)
+        W = np.stack([C, np.roll(C, 1, axis=0)])
+        y = pwq.quantized_matmul_fp8_grouped(x.view(torch.float8_e4m3fn), as_scales(sx), e4m3(W), as_scales(np.stack([sw, sw])),
+                                             torch.from_numpy(off).to(DEV), rows=torch.from_numpy(at[pick].astype(np.int32)).to(DEV),
+                                             out_dtype=TYPES[out])
+        for e in range(2):
+            i = pick[off[e]:off[e + 1]]
+            check_product(y[off[e]:off[e + 1]], X[i], np.ones((9, len(i)), dtype=np.float32), W[e], sw, TYPES[out])
+
+
+def test_workspaces(pwq):
+    """A product that splits k: the same result with the caller's workspace, whatever it held, or without one."""
+    rng = np.random.default_rng(13)
+    T, n, m = 3, 8208, 40
+    X, C = random_codes(rng, T, n), random_codes(rng, m, n)
+    sx, sw = random_scales(rng, False, 65, T), random_scales(rng, False, 1, 65)
+    args = (e4m3(X), as_scales(sx), e4m3(C), as_scales(sw))
+    need = pwq.lib().pwq_quantized_matmul_fp8_workspace_size(T, n, m)
+    assert need > 0
+    one = pwq.quantized_matmul_fp8(*args, out_dtype=torch.float32)
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+    two = pwq.quantized_matmul_fp8(*args, out_dtype=torch.float32, ws=ws)
+    assert torch.equal(one, two)
+    check_product(one, X, sx, C, sw, torch.float32)
+    with pytest.raises(pwq.PwqError):
+        pwq.quantized_matmul_fp8(*args, ws=ws[:-1])
+    with pytest.raises(pwq.PwqError):
+        pwq.quantized_matmul_fp8(*args, ws=torch.empty(need + 4, dtype=torch.uint8, device=DEV)[4:])
+    with pytest.raises(ValueError):
+        pwq.quantized_matmul_fp8(*args, ws=ws.cpu())
+
+
 # ------------------------------------------------------------------ as they are used
 def _layer(pwq, rng, E, n, m, st):
     W = torch.from_numpy((rng.standard_normal((E, m, n)) * 0.05).astype(np.float32)).to(torch.bfloat16).to(DEV)
