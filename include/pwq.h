@@ -537,14 +537,15 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *             formats above, both scales of scale_type.
  *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy.
  *   ws        pwq_quantized_matmul_fp8_workspace_size(n_tok, d_in, d_out) bytes, 16-byte aligned (0
- *             bytes: ws may be NULL): the float32 sums of a split k.
+ *             bytes: ws may be NULL): the float32 sums of a split k and, where d_in is no multiple of
+ *             16 and there are rows enough, copies of X and of the codes (about as many bytes as they).
  * A block's sum over k is multiplied by the product of its two scales, formed in float32, and added to a
  * float32 sum.  With float32 Y that sum over k is of exact products in float32.  With 16-bit Y it may come
  * from the e4m3 matrix instruction, which of each eight consecutive products keeps what is at least 2^-13
  * of the largest: off by less than 2^-10 of the largest of each eight (about 5e-5 of the result's norm on
  * normal data, a rounding to float16 2e-4).
  * Any alignment and sizes; rows of X and codes that start at multiples of 16 bytes take the faster
- * kernels.  Codes of NaN and scales of NaN give NaN.
+ * kernels, as do the copies of rows of other lengths.  Codes of NaN and scales of NaN give NaN.
  *
  * pwq_quantized_matmul_fp8_grouped: the product of a layer of experts.  n_rows output rows are sorted
  * by expert: those of expert e are offsets[e] .. offsets[e + 1] - 1, any number of them.

@@ -46,6 +46,7 @@ struct F8Args {
     int64_t xrows, kper;           // X's rows; k per split
     int experts, groups, splits, y_dtype;
     int tiles_t, tiles_m;
+    bool laid;                     // X is a copy, a row for each output row
 };
 
 // ------------------------------------------------------------------ which rows
@@ -553,7 +554,7 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
         o0 = (int64_t)to * BO;
         rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
         cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
-        xbase = a.X + (a.rows ? 0 : at.t0 * a.ldx) + kbeg;
+        xbase = a.X + (a.rows && !a.laid ? 0 : at.t0 * a.ldx) + kbeg;
         cbuf = f8_buffer(TWO && grp == 1 ? xbase : cbase);
         xbuf = f8_buffer(xbase);                          // two stages: a wave copies rows of one operand alone, cbuf's
 #pragma unroll
@@ -562,7 +563,7 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
             const int ch = f8_pos(r & 15, lane & 7);      // the xor undoes itself
             if (of_x(j)) {
                 const int64_t t = at.t0 + r - BO < at.end ? at.t0 + r - BO : at.end - 1;
-                off[j] = (uint32_t)((a.rows ? f8_xrow(a, t) : t - at.t0) * a.ldx + 16 * ch);
+                off[j] = (uint32_t)((a.rows && !a.laid ? f8_xrow(a, t) : t - at.t0) * a.ldx + 16 * ch);
             } else {
                 off[j] = (uint32_t)((o0 + r < a.m ? r : a.m - 1 - o0) * a.n + 16 * ch);
             }
@@ -965,7 +966,7 @@ __global__ __launch_bounds__(64 * W) void f8_row_kernel(F8Args a) {
     const bool xin = t < at.end;
     const int64_t xt = f8_xrow(a, xin ? t : at.end - 1);
     const uint8_t* crow = a.C + ((int64_t)at.expert * a.m + (o0 + r < a.m ? o0 + r : a.m - 1)) * a.n + 16 * c;
-    const uint8_t* xrow = a.X + xt * a.ldx + 16 * c;
+    const uint8_t* xrow = a.X + (a.laid ? (xin ? t : at.end - 1) : xt) * a.ldx + 16 * c;
     const int64_t wat = f8_sw_at(a, at.expert, o0, 0);
     const bool bad = xin && f8_bad(a, t);
     struct Turn {
@@ -1068,6 +1069,41 @@ __global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
     }
 }
 
+// ------------------------------------------------------------------ copies
+// X's row of each output row, and behind them the codes' rows, to rows of a multiple of 16 bytes with
+// zeros at the end: 256 chunks of 16 bytes a wave at a time, four a lane.  The chunk that a row ends in
+// is the row's last 16 bytes, moved down.  n >= 16, fewer than 2^30 chunks a row.  Memory's rate bounds
+// it: 8000 + 1001 rows of 28671 in 88 us, 5.8 TB/s; with a wave to a row short rows took twice as long
+// (64 x 2049 + 16000 rows of 1025: 104 us, now 50).
+__global__ __launch_bounds__(256) void f8_lay_kernel(F8Args a, uint8_t* X, uint8_t* C) {
+    const int64_t ld = f8_laid(a.n), chunks = (a.T + (int64_t)a.experts * a.m) * (ld / 16);
+    const uint32_t cpr = (uint32_t)(ld / 16);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t at = ((int64_t)blockIdx.x * 4 + wave) * 256; at < chunks; at += (int64_t)gridDim.x * 1024) {
+        const int64_t row0 = at / cpr;
+        const uint32_t first = (uint32_t)(at - row0 * cpr);
+        uint4 v[4];
+        uint8_t* to[4];
+        int drop[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t c = first + 64 * u + lane, down = c / cpr;
+            const bool in = at + 64 * u + lane < chunks;
+            const int64_t i = in ? row0 + down : 0, k = in ? 16 * (int64_t)(c - down * cpr) : 0;
+            const int64_t past = k + 16 - a.n;
+            drop[u] = past < 0 ? 0 : (int)past;
+            const uint8_t* p = (i < a.T ? a.X + f8_xrow(a, i) * a.ldx : a.C + (i - a.T) * a.n) + (k - drop[u]);
+            __builtin_memcpy(&v[u], p, 16);
+            to[u] = in ? (i < a.T ? X + i * ld : C + (i - a.T) * ld) + k : nullptr;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (drop[u]) v[u] = f8_drop(v[u], drop[u]);
+            if (to[u]) *(uint4*)to[u] = v[u];
+        }
+    }
+}
+
 // ------------------------------------------------------------------ launches
 template <int BO, int BT, int NST, int WO, int KG, bool EXACT>
 hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
@@ -1134,7 +1170,16 @@ hipError_t f8_launch(const F8Call& c, hipStream_t s) {
     const bool near = c.n < ((int64_t)1 << 24) && (c.rows ? c.xrows * c.ldx < ((int64_t)1 << 32) : c.ldx < ((int64_t)1 << 24));
     const bool fast = c.n % 16 == 0 && c.ldx % 16 == 0 && aligned(c.X, 16) && aligned(c.C, 16) && near;
     const bool exact = c.y_dtype == 0;
-    return f8_run(a, c.e8, exact, f8_plan(F8Shape{c.T, c.n, c.m, c.experts, exact, fast}), s);
+    const F8Plan p = f8_plan(F8Shape{c.T, c.n, c.m, c.experts, exact, fast});
+    if (p.lay) {
+        uint8_t* const X = (uint8_t*)c.ws + f8_plan_ws_sums(p, c.T, c.m);
+        uint8_t* const C = X + c.T * f8_laid(c.n);
+        const int64_t blocks = cdiv((c.T + c.experts * c.m) * (f8_laid(c.n) / 16), 1024);
+        hipLaunchKernelGGL(f8_lay_kernel, dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, s, a, X, C);
+        if (const hipError_t e = hipGetLastError()) return e;
+        a.X = X; a.C = C; a.ldx = a.n = f8_laid(c.n); a.laid = true;
+    }
+    return f8_run(a, c.e8, exact, p, s);
 }
 
 }  // namespace pwq

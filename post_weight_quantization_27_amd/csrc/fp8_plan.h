@@ -17,6 +17,8 @@ struct F8Plan {
     int kind;                      // one of the below, an index into f8_tiles, or F8_ANY + one into f8_any
     int splits;
     int64_t kper;
+    double us = 0.0;               // estimate
+    bool lay = false;              // the operands are copied to rows of 16-byte multiples first
 };
 constexpr int F8_ROW1 = -1, F8_ROW2 = -2, F8_ANY = 8;
 
@@ -90,6 +92,7 @@ inline F8Plan f8_plan_any(const F8Shape& s) {
             if (t < least) { least = t; best = p; }
         }
     }
+    best.us = least;
     return best;
 }
 
@@ -115,8 +118,7 @@ constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 // and scale type): the choice takes 2.0 % longer than the fastest kernel in the geometric mean and 32 % at
 // the worst (192 rows by 768 x 768: 7.3 against 5.5 us); 128 x 128 tiles alone take 58 % longer in the
 // mean and up to 5.8 times as long.
-inline F8Plan f8_plan(const F8Shape& s) {
-    if (!s.fast) return f8_plan_any(s);
+inline F8Plan f8_plan_fast(const F8Shape& s) {
     const F8Shares e = f8_shares(s.T, s.experts);
     const double bytes = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6;      // MB
     const double mem = bytes / 5.0 + 2.7;
@@ -145,9 +147,31 @@ inline F8Plan f8_plan(const F8Shape& s) {
         const double t1 = 3.2 + 0.74 * one + 0.695 * (double)f8_cdiv(s.n, 1024);
         const double t2 = 3.2 + 0.909 * one + 0.255 * (double)f8_cdiv(s.n, 2048);
         if (t1 < least) { least = t1; best = f8_split(F8_ROW1, s.n, 1); }
-        if (t2 < least) best = f8_split(F8_ROW2, s.n, 1);
+        if (t2 < least) { least = t2; best = f8_split(F8_ROW2, s.n, 1); }
     }
+    best.us = least;
     return best;
+}
+
+// d_in of the copies whose rows are multiples of 16 bytes
+constexpr int64_t f8_laid(int64_t n) { return (n + 15) / 16 * 16; }
+
+// The kernel of a call.  Rows of any length are copied to rows of 16-byte multiples first where that and
+// the faster kernels are estimated to take less than the kernels for any alignment: a launch and the bytes
+// at 6 TB/s.  8000 rows by 8191 x 8191, bfloat16: 488 us with 42 of copies, 1367 without; 700 by 4099 x
+// 4111: 39 and 49; 128 by 4099 x 4111: 25 and 21.  Over 90 shapes with odd d_in (32 .. 10000 rows) the
+// choice takes 0.1 % longer than the better of the two in the mean and 6 % at the worst, no copies 11 %
+// and up to 2.5 times as long.
+inline F8Plan f8_plan(const F8Shape& s) {
+    if (s.fast) return f8_plan_fast(s);
+    const F8Plan any = f8_plan_any(s);
+    if (s.n % 16 == 0 || s.n < F8_STEP || s.n >= ((int64_t)1 << 24) - 16) return any;
+    F8Shape l = s;
+    l.n = f8_laid(s.n);
+    F8Plan p = f8_plan_fast(l);
+    p.us += 6.0 + 2e-6 * ((double)s.T + (double)s.experts * s.m) * (double)s.n / 6.0;
+    p.lay = true;
+    return p.us < any.us ? p : any;
 }
 
 inline bool f8_plan_size_ok(int64_t T, int64_t m, int64_t experts) {
@@ -155,14 +179,20 @@ inline bool f8_plan_size_ok(int64_t T, int64_t m, int64_t experts) {
     return f8_tiles_most(T, experts, 64) * f8_cdiv(m, 64) < ((int64_t)1 << 23) && f8_cdiv(m, 16) < ((int64_t)1 << 23);
 }
 
+// The workspace: the splits' sums, and behind them the copies of X's rows and of the codes
+inline size_t f8_plan_ws_sums(const F8Plan& p, int64_t T, int64_t m) {
+    return p.splits > 1 ? ((size_t)p.splits * (size_t)T * (size_t)m * sizeof(float) + 15) / 16 * 16 : 0;
+}
 inline size_t f8_plan_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts) {
     // the outputs' type, and where rows start, are the call's affair: room for any of its plans
-    int most = 1;
+    size_t most = 0;
     for (int i = 0; i < (n % 16 == 0 ? 4 : 2); ++i) {
         const F8Plan p = f8_plan(F8Shape{T, n, m, experts, (i & 1) != 0, (i & 2) != 0});
-        most = p.splits > most ? p.splits : most;
+        const size_t copies = p.lay ? ((size_t)T + (size_t)experts * (size_t)m) * (size_t)f8_laid(n) : 0;
+        const size_t b = f8_plan_ws_sums(p, T, m) + copies;
+        most = b > most ? b : most;
     }
-    return most > 1 ? (size_t)most * (size_t)T * (size_t)m * sizeof(float) : 0;
+    return most;
 }
 
 }  // namespace pwq

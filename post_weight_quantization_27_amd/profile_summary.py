@@ -54,6 +54,8 @@ CALL_OF = [
     ("mse_", "recon_mse"), ("EpiSq", "recon_mse"), ("set_double", "recon_mse"),
     ("SplitTriMap", "recon_mse"), ("EpiTrace", "recon_mse"),
     ("w4a16", "quantized_matmul"), ("w8_", "quantized_matmul_int8"), ("tok_", "quantize_tokens, rms_norm_quantize"),
+    ("f8_tokens", "quantize_tokens_fp8"), ("f8_blocks", "quantize_blocks_fp8"),
+    ("f8_", "quantized_matmul_fp8, quantized_matmul_fp8_grouped"),
     ("chan_abs", "channel_abs_mean"), ("chan_mean", "channel_abs_mean"),
     ("awq_", "awq_search"), ("EpiDot", "awq_search"),
     ("tensor_max", "tensor_scales"), ("tensor_scale", "tensor_scales"),

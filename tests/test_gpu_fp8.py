@@ -375,6 +375,33 @@ def test_grouped_bad_indexes_and_offsets(pwq):
     assert (Y[30:] == 7).all()
 
 
+def test_copied_operands_of_odd_rows(pwq):
+    """Sizes whose operands are copied first: codes of NaN between X's rows are not read as values, a row with
+    an index outside X is NaN, and rows outside the offsets are left alone."""
+    rng = np.random.default_rng(8)
+    n, m, E, T, n_x = 557, 1879, 2, 2200, 1100
+    X, C = random_codes(rng, n_x, n), random_codes(rng, E, m, n)
+    sx, sw = random_scales(rng, False, 5, n_x), random_scales(rng, False, E, 15, 5)
+    wide = torch.full((n_x, n + 6), 0x7F, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    wide.view(torch.uint8)[:, 2:n + 2] = torch.from_numpy(X).to(DEV)
+    rows = rng.integers(0, n_x, T).astype(np.int32)
+    rows[[3, 1500]] = [n_x, -7]
+    for out in (torch.bfloat16, torch.float32):
+        Y = torch.full((T, m), 7.0, dtype=out, device=DEV)
+        pwq.quantized_matmul_fp8_grouped(wide[:, 2:n + 2], as_scales(sx), e4m3(C), as_scales(sw),
+                                         torch.tensor([1, 1200, T - 1], dtype=torch.int32, device=DEV),
+                                         rows=torch.from_numpy(rows).to(DEV), out=Y)
+        assert torch.isnan(Y[[3, 1500]]).all() and int(torch.isnan(Y).sum()) == 2 * m
+        assert (Y[0] == 7).all() and (Y[-1] == 7).all()
+        for e, i in ((0, [1, 2, 700, 1199]), (1, [1200, 1501, T - 2])):
+            for b in (0, 14):
+                o = slice(128 * b, min(m, 128 * b + 128))
+                check_product(Y[i][:, o], X[rows[i]], sx[:, rows[i]], C[e][o], sw[e][b:b + 1], out)
+        y = pwq.quantized_matmul_fp8(wide[:, 2:n + 2], as_scales(sx), e4m3(C)[0], as_scales(sw)[0], out_dtype=out)
+        assert torch.isfinite(y).all()
+        check_product(y[-3:, -87:], X[-3:], sx[:, -3:], C[0][-87:], sw[0][14:], out)
+
+
 def test_grouped_offsets_in_any_order_stay_inside(pwq):
     """Offsets that decrease: whatever the rows become, nothing outside them is written."""
     rng = np.random.default_rng(7)

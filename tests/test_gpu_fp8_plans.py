@@ -25,6 +25,13 @@ PRODUCTS = [  # rows, d_in, d_out, experts
     (700, 1041, 2056, 6), (1030, 1041, 2056, 6), (1600, 1041, 520, 6), (1600, 2065, 520, 6), (1600, 4113, 72, 6), (1600, 401, 5512, 6),
 ]
 
+# rows of any length that are copied to rows of 16-byte multiples first
+LAID = [
+    (2208, 131, 4037, 1), (371, 13409, 649, 1), (2031, 557, 1879, 1), (869, 139, 7308, 1), (1, 81505, 1, 1), (903, 4627, 521, 1),
+    (853, 2641, 1192, 1), (3174, 135, 2628, 6), (4872, 1431, 535, 6), (3779, 7455, 330, 6), (4344, 277, 1489, 6), (1, 82425, 1, 6),
+    (276, 3093, 1, 130), (385, 48235, 270, 1),
+]
+
 
 def values(codes, sx):
     s = sx.float().double().cpu().to(DEV) if sx.element_size() == 4 else torch.exp2(sx.view(torch.uint8).double() - 127)
@@ -32,7 +39,7 @@ def values(codes, sx):
 
 
 @pytest.mark.parametrize("out,scales", [("bf16", "f32"), ("f32", "f32"), ("f16", "e8m0"), ("f32", "e8m0")])
-@pytest.mark.parametrize("T,n,m,E", PRODUCTS)
+@pytest.mark.parametrize("T,n,m,E", PRODUCTS + LAID)
 def test_kernels(pwq, T, n, m, E, out, scales):
     rng = np.random.default_rng(T + n + m + E)
     G, OB, dt = -(-n // 128), -(-m // 128), TYPES[out]
