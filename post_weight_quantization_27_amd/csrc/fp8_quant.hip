@@ -29,7 +29,7 @@ struct F8QuantArgs {
     void* S;                       // float32 or e8m0
     int64_t ldx, ldq, lds, T;      // tokens, or rows of a matrix; lds: the tokens' scales' pitch
     int64_t stride;                // between matrices
-    int64_t tiles, tiles_t;
+    int64_t tiles, tiles_t, tiles_g;
     int64_t mats;
     int d, groups, tshift;
 };
@@ -135,28 +135,41 @@ __device__ __forceinline__ void f8_store(uint8_t* q, int col, int d, const uint3
     }
 }
 
+// a / b, in 32 bits where they fit
+__device__ __forceinline__ int64_t f8q_div(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // ------------------------------------------------------------------ tokens
 // 16 lanes hold a token's 128 values, eight each.  A workgroup takes 2^tshift tokens (16, fewer where
-// there are fewer) by 16 / 2^tshift groups in turn, F8Q_TURNS of them, so that the scales of 16 tokens
-// are written in one piece and all loads are under way before the first maximum.
-constexpr int F8Q_TURNS = 4;
+// there are fewer) by 16 / 2^tshift groups in U turns, so that the scales of 16 tokens are written in
+// one piece and all loads are under way before the first maximum.  Workgroups go through a row's groups
+// first: through the tokens first 8192 x 8192 takes 49 us in place of 44 (rows 16 KB apart meet in the
+// same memory channels).
+//
+// U is 1 where workgroups are few or a row is one turn (16 x 8192 2.9 us, 3.8 with two and 5.0 with four
+// turns; 100000 x 128 12.9, 13.8 and 15.5); else 2 for float32 scales on aligned rows and 4 otherwise
+// (bfloat16: 4096 x 28672 72.5 us with two, 74.6 with four and 83.5 with one; 4096 x 28671 89, 79 and 93;
+// float16, powers of two: 4096 x 28672 66.5, 63.4 and 66.6).
+constexpr int64_t F8Q_FEW = 16 * 256;
 
-template <int XT, int AL, bool E8>
+template <int XT, int AL, bool E8, int U>
 __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
     const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
     const int wide = 16 >> a.tshift;                      // groups side by side
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        const int64_t t = ((tile % a.tiles_t) << a.tshift) + (sub & ((1 << a.tshift) - 1));
-        const int g0 = (int)(tile / a.tiles_t) * (wide * F8Q_TURNS) + (sub >> a.tshift);
+        const int64_t tt = f8q_div(tile, a.tiles_g);
+        const int64_t t = (tt << a.tshift) + (sub & ((1 << a.tshift) - 1));
+        const int g0 = (int)(tile - tt * a.tiles_g) * (wide * U) + (sub >> a.tshift);
         const char* row = (const char*)a.X + (t < a.T ? t : a.T - 1) * a.ldx * Raw<XT>::SIZE;
-        Raw<XT> x[F8Q_TURNS];
+        Raw<XT> x[U];
 #pragma unroll
-        for (int u = 0; u < F8Q_TURNS; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t col = (int64_t)(g0 + u * wide) * F8_B + 8 * l;
             x[u].template fetch<AL>(row, (int)(col < a.d ? col : a.d), a.d);
         }
 #pragma unroll
-        for (int u = 0; u < F8Q_TURNS; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int g = g0 + u * wide;
             const int64_t col64 = (int64_t)g * F8_B + 8 * l;
             const int col = (int)(col64 < a.d ? col64 : a.d);
@@ -183,8 +196,8 @@ __global__ __launch_bounds__(256) void f8_blocks_kernel(F8QuantArgs a) {
     const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
     int par = 0;
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, par ^= 1) {
-        const int g = (int)(tile % a.groups);
-        const int64_t rest = tile / a.groups, ob = rest % a.tiles_t, mat = rest / a.tiles_t;
+        const int64_t rest = f8q_div(tile, a.groups), mat = f8q_div(rest, a.tiles_t), ob = rest - mat * a.tiles_t;
+        const int g = (int)(tile - rest * a.groups);
         const char* base = (const char*)a.X + mat * a.stride * Raw<XT>::SIZE;
         const int col = g * F8_B + 8 * l;                 // d is below 2^30 + 128
         Raw<XT> x[8];
@@ -220,23 +233,30 @@ __global__ __launch_bounds__(256) void f8_blocks_kernel(F8QuantArgs a) {
 // ------------------------------------------------------------------ launches
 constexpr int64_t F8Q_MAX_GROUPS = 1 << 20;               // tiles past this are taken by the kernel's loop
 
-template <int XT, int AL, bool TOKENS>
-void f8q_go(const F8QuantArgs& a, bool e8, hipStream_t s) {
+template <int XT, int AL, bool E8, int U>
+void f8q_tokens(F8QuantArgs a, hipStream_t s) {
+    a.tiles_g = cdiv(a.groups, (16 >> a.tshift) * U);
+    a.tiles = a.tiles_t * a.tiles_g;
     const dim3 grid((unsigned)(a.tiles < F8Q_MAX_GROUPS ? a.tiles : F8Q_MAX_GROUPS));
+    hipLaunchKernelGGL((f8_tokens_kernel<XT, AL, E8, U>), grid, dim3(256), 0, s, a);
+}
+template <int XT, int AL, bool E8, bool TOKENS>
+void f8q_go(const F8QuantArgs& a, hipStream_t s) {
     if constexpr (TOKENS) {
-        if (e8) hipLaunchKernelGGL((f8_tokens_kernel<XT, AL, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((f8_tokens_kernel<XT, AL, false>), grid, dim3(256), 0, s, a);
+        const int64_t turns = cdiv(a.groups, 16 >> a.tshift);
+        if (AL == ROWS_SHORT || turns == 1 || a.tiles_t * turns <= F8Q_FEW) f8q_tokens<XT, AL, E8, 1>(a, s);
+        else if constexpr (AL != ROWS_SHORT) f8q_tokens<XT, AL, E8, AL == ROWS_VEC && !E8 ? 2 : 4>(a, s);
     } else {
-        if (e8) hipLaunchKernelGGL((f8_blocks_kernel<XT, AL, true>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((f8_blocks_kernel<XT, AL, false>), grid, dim3(256), 0, s, a);
+        const dim3 grid((unsigned)(a.tiles < F8Q_MAX_GROUPS ? a.tiles : F8Q_MAX_GROUPS));
+        hipLaunchKernelGGL((f8_blocks_kernel<XT, AL, E8>), grid, dim3(256), 0, s, a);
     }
 }
 template <int XT, bool TOKENS>
 void f8q_rows(const F8QuantArgs& a, bool e8, hipStream_t s) {
     const bool vec = a.d % 8 == 0 && a.ldx % 8 == 0 && a.ldq % 8 == 0 && a.stride % 8 == 0 && aligned(a.X, 16) && aligned(a.Q, 8);
-    if (vec) f8q_go<XT, ROWS_VEC, TOKENS>(a, e8, s);
-    else if (a.d >= 8) f8q_go<XT, ROWS_ANY, TOKENS>(a, e8, s);
-    else f8q_go<XT, ROWS_SHORT, TOKENS>(a, e8, s);
+    if (vec) (e8 ? f8q_go<XT, ROWS_VEC, true, TOKENS>(a, s) : f8q_go<XT, ROWS_VEC, false, TOKENS>(a, s));
+    else if (a.d >= 8) (e8 ? f8q_go<XT, ROWS_ANY, true, TOKENS>(a, s) : f8q_go<XT, ROWS_ANY, false, TOKENS>(a, s));
+    else (e8 ? f8q_go<XT, ROWS_SHORT, true, TOKENS>(a, s) : f8q_go<XT, ROWS_SHORT, false, TOKENS>(a, s));
 }
 template <bool TOKENS>
 hipError_t f8q_run(const F8QuantArgs& a, int x_dtype, bool e8, hipStream_t s) {
@@ -255,7 +275,6 @@ hipError_t f8_tokens_launch(const void* X, int x_dtype, int64_t T, int64_t d, in
     a.groups = (int)cdiv(d, F8_B);
     while (a.tshift < 4 && (1 << a.tshift) < T) ++a.tshift;
     a.tiles_t = cdiv(T, 1 << a.tshift);
-    a.tiles = a.tiles_t * cdiv(a.groups, (16 >> a.tshift) * F8Q_TURNS);
     return f8q_run<true>(a, x_dtype, e8, s);
 }
 

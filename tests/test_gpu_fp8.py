@@ -97,6 +97,20 @@ def test_tokens_strided(pwq, scales):
         assert (codes[:, :off] == 7).all() and (codes[:, off + d:] == 7).all() and (raw(s[:, T:]) == 7).all()
 
 
+@pytest.mark.parametrize("scales", list(SCALES))
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,d", [(2101, 4104), (2101, 4099), (70001, 129)])
+def test_many_tokens(pwq, T, d, dtype, scales):
+    """Workgroups that take groups in several turns: the same as few tokens at a time, which take one."""
+    x = hidden(np.random.default_rng(d), 700, d, dtype).repeat(-(-T // 700), 1)[:T]
+    x += torch.arange(T, device=DEV).remainder(37).to(x.dtype)[:, None] / 16
+    r = pwq.quantize_tokens_fp8(x, scale_dtype=SCALES[scales])
+    for t in range(0, T, 700):
+        few = [pwq.quantize_tokens_fp8(x[u:min(u + 100, T)], scale_dtype=SCALES[scales]) for u in range(t, min(t + 700, T), 100)]
+        assert np.array_equal(raw(r["codes"][t:t + 700]), np.concatenate([raw(f["codes"]) for f in few]))
+        assert np.array_equal(raw(r["scales"][:, t:t + 700]), np.concatenate([raw(f["scales"]) for f in few], axis=1))
+
+
 def special_rows():
     """Blocks that are hard to round: ties, borders, tiny and huge values, zeros, NaN and infinities."""
     rng = np.random.default_rng(1)
