@@ -122,22 +122,21 @@ __device__ __forceinline__ bool f8_bad(const F8Args& a, int64_t t) {
 // shares are of the tiles that hold rows: of those that might, which are launched, the last ones hold none
 // (32768 rows of 64 experts by 4096 x 4096: 708 us with shares of all).
 template <int BT>
-__device__ __forceinline__ bool f8_tile(const F8Args& a, int64_t bid, int& to, F8Rows& r) {
+__device__ __forceinline__ bool f8_tile(const F8Args& a, uint32_t bid, int& to, F8Rows& r) {
     F8Count<BT> c;
-    int64_t tiles_t = a.tiles_t;
+    uint32_t tiles_t = (uint32_t)a.tiles_t;
     if (a.offsets) {
         tiles_t = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 64) tiles_t += c.of(a, e0);
+        for (int e0 = 0; e0 < a.experts; e0 += 64) tiles_t += (uint32_t)c.of(a, e0);
     }
-    const int64_t nt = tiles_t * a.tiles_m;
+    const uint32_t nt = tiles_t * (uint32_t)a.tiles_m;    // below 2^24 (f8_plan_size_ok)
     if (bid >= nt) return false;
-    const int64_t x = bid & 7, per = nt >> 3, rem = nt & 7;
-    const int64_t id = x * per + (x < rem ? x : rem) + (bid >> 3);
-    const int64_t band = 8 * tiles_t, g = id / band;
-    const int rows = a.tiles_m - 8 * g < 8 ? (int)(a.tiles_m - 8 * g) : 8;
-    const int in = (int)(id - g * band);
-    const int tt = in / rows;
-    to = (int)(8 * g) + in - tt * rows;
+    const uint32_t x = bid & 7, per = nt >> 3, rem = nt & 7;
+    const uint32_t id = x * per + (x < rem ? x : rem) + (bid >> 3);
+    const uint32_t band = 8 * tiles_t, g = id / band, left = (uint32_t)a.tiles_m - 8 * g;
+    const uint32_t rows = left < 8 ? left : 8, in = id - g * band, down = in / rows;
+    const int tt = (int)down;
+    to = (int)(8 * g + in - down * rows);
     if (a.offsets && a.experts <= 64) c.find(0, tt, r);
     else r = f8_rows<BT>(a, tt);
     return r.t0 < r.end;
@@ -548,11 +547,11 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     // memory channels.  Large token tiles share X by k instead and start together.
     constexpr int ROT = BT <= 128 ? 3 : 0;
     int rot;
-    auto setup = [&](int64_t tile) {
+    auto setup = [&](uint32_t tile) {
         int to;
         if (!f8_tile<BT>(a, tile, to, at)) return false;
         o0 = (int64_t)to * BO;
-        rot = ROT && nfull > 0 ? (int)(((int64_t)to * ROT) % nfull) : 0;
+        rot = ROT && nfull > 0 ? (int)((uint32_t)(to * ROT) % (uint32_t)nfull) : 0;
         cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
         xbase = a.X + (a.rows && !a.laid ? 0 : at.t0 * a.ldx) + kbeg;
         cbuf = f8_buffer(TWO && grp == 1 ? xbase : cbase);
@@ -757,8 +756,8 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
                 if (q == (2 * (j - from) + 1) * Q / (2 * (to - from))) copy_some(it, j, j + 1);
         };
     };
-    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_m;
-    int64_t tile = blockIdx.x;
+    const uint32_t tiles = (uint32_t)a.tiles_t * (uint32_t)a.tiles_m;
+    uint32_t tile = blockIdx.x;
     auto next = [&] {                                     // the first stages of the next tile that has rows
         if (tile >= tiles || !setup(tile)) return false;
         if constexpr (TWO) {
