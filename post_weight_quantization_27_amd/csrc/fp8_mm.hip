@@ -30,8 +30,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int F8_CUS = 256;                // compute units (a multiple of the 8 XCDs)
-
 struct F8Args {
     const uint8_t* X;
     const void* sx;                // groups x X's rows, pitch ldsx: float32 or e8m0
@@ -488,10 +486,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base)
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00027000);
 }
 
-// One workgroup per compute unit that goes through its tiles, where the registers allow it
-template <int BO, int BT, int KG>
-constexpr bool f8_persist = KG == 1 && BO * BT < 65536;
-
 template <int BO, int BT, int NST, int WO, int KG, bool E8, bool EXACT>
 __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     constexpr int BK = F8_B, NW = 8 / KG, WT = NW / WO;   // waves that share a stage
@@ -502,7 +496,6 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     constexpr bool TWO = NST == 2;
     constexpr int SLOT = (BO + BT) * BK, ST = SLOT + NW * 256;
     constexpr int NB = BO > F8_B ? BO / F8_B : 1;         // blocks of outputs
-    constexpr bool PERSIST = f8_persist<BO, BT, KG>;
     static_assert(L * NW * 8 == BO + BT && BO % (NW * 8) == 0 && (L + 1) * (NST - 1) < 64 && KG * NST * ST <= 163840, "tile");
     static_assert(BO / WO <= F8_B && BT % 64 == 0 && BT / 64 < NW, "scales");
     static_assert(KG == 1 || (NST > 2 && FO % 2 == 0 && 8 * FO / 2 * FT * 1024 <= 2 * NST * ST), "the groups' sums fit the stages");
@@ -672,21 +665,24 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
         }
         read();
         f8_wait_lds();
-        f16x8 ho[EXACT ? FP : 1][4], ht[EXACT ? FT : 1][4];
+        // float16 operands: the tokens' and the first row's here, a later row's under the instructions of the
+        // one before it, which leaves the registers for tiles of 256 x 128
+        f16x8 ho[EXACT ? 2 : 1][4], ht[EXACT ? FT : 1][4];
+        auto half_row = [&](int i) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) ho[i & 1][h] = f8_half(fo[i][2 * h], fo[i][2 * h + 1]);
+        };
         if constexpr (EXACT) {
+            // waited for above: no use of them moves up
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int i = 0; i < FP; ++i) asm volatile("" : "+v"(fo[i]));
 #pragma unroll
-                for (int i = 0; i < FP; ++i) {
-                    asm volatile("" : "+v"(fo[i]));       // waited for above: no use of it moves up
-                    ho[i][h] = f8_half(fo[i][2 * h], fo[i][2 * h + 1]);
-                }
+            for (int j = 0; j < FT; ++j) {
+                asm volatile("" : "+v"(ft[j]));
 #pragma unroll
-                for (int j = 0; j < FT; ++j) {
-                    asm volatile("" : "+v"(ft[j]));
-                    ht[j][h] = f8_half(ft[j][2 * h], ft[j][2 * h + 1]);
-                }
+                for (int h = 0; h < 4; ++h) ht[j][h] = f8_half(ft[j][2 * h], ft[j][2 * h + 1]);
             }
+            half_row(0);
         }
         f8_barrier();
         __builtin_amdgcn_s_setprio(1);
@@ -710,7 +706,8 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
                 r = (f32x4){0.f, 0.f, 0.f, 0.f};
                 if constexpr (EXACT) {
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) r = __builtin_amdgcn_mfma_f32_16x16x32_f16(ho[q / FT][h], ht[q % FT][h], r, 0, 0, 0);
+                    for (int h = 0; h < 4; ++h) r = __builtin_amdgcn_mfma_f32_16x16x32_f16(ho[(q / FT) & 1][h], ht[q % FT][h], r, 0, 0, 0);
+                    if (q % FT == 0 && q / FT + 1 < FP) half_row(q / FT + 1);
                 } else {
                     r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fo[q / FT], ft[q % FT], r, 0, 0, 0, 0, 0, 0);
                 }
@@ -756,194 +753,180 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
                 if (q == (2 * (j - from) + 1) * Q / (2 * (to - from))) copy_some(it, j, j + 1);
         };
     };
-    const uint32_t tiles = (uint32_t)a.tiles_t * (uint32_t)a.tiles_m;
-    uint32_t tile = blockIdx.x;
-    auto next = [&] {                                     // the first stages of the next tile that has rows
-        if (tile >= tiles || !setup(tile)) return false;
-        if constexpr (TWO) {
-            copy_some(0, 0, L + 1);
-            copy_some(1, 0, grp == 0 ? 5 : L + 1);
+    // the first stages
+    if (!setup(blockIdx.x)) return;
+    if constexpr (TWO) {
+        copy_some(0, 0, L + 1);
+        copy_some(1, 0, grp == 0 ? 5 : L + 1);
+    } else {
+        for (int q = 0; q < NST - 1; ++q) copy_some(q, 0, L + 1);
+        if (INSIDE && (KG == 2 || grp == 1)) copy_some(NST - 1, 0, L + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < FO; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    if constexpr (!INSIDE) {
+#pragma unroll
+        for (int q = 0; q <= AHEAD; ++q) p[q] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < FT; ++j) s[j] = 0.f;
+    }
+    if constexpr (TWO) {
+        // Quarter steps 4 s and 4 s + 2: the first group reads of stage s; 4 s + 1 and 4 s + 3: the
+        // second.  X and the scales of stage s are read by quarter 4 s + 1, the codes of the first
+        // parts by 4 s + 1, of the second by 4 s + 3.  Stage s + 2 takes their place:
+        //   codes: copies 0 .. 3 and the scales' in quarter 4 s + 3, 4 .. 7 in 4 s + 5 (with the reads
+        //   4 s + 2 and 4 s + 4); read from 4 s + 8 and 4 s + 10 on, so all but a wave's last 9 have
+        //   landed when it waits, after its instructions;
+        //   X: copies 0 .. 3 and the scales' in 4 s + 2, 4 .. 7 in 4 s + 4 (with the reads all in 4 s + 3);
+        //   read from 4 s + 8 on: the wait, in the reads of 4 s + 7, leaves 5 (ahead of the copies: 0).
+        static_assert(!TWO || (L == 8 && KG == 1 && BO == 256 && BT == 256), "two stages");
+        if (nk > 1) {
+            if (grp == 0) f8_wait_vm<5>();
+            else f8_wait_vm<9>();
         } else {
-            for (int q = 0; q < NST - 1; ++q) copy_some(q, 0, L + 1);
-            if (INSIDE && (KG == 2 || grp == 1)) copy_some(NST - 1, 0, L + 1);
+            f8_wait_vm<0>();
         }
-        return true;
-    };
-    if (!next()) return;
-    for (;;) {
-#pragma unroll
-        for (int i = 0; i < FO; ++i)
-#pragma unroll
-            for (int j = 0; j < FT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        if constexpr (!INSIDE) {
-#pragma unroll
-            for (int q = 0; q <= AHEAD; ++q) p[q] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < FT; ++j) s[j] = 0.f;
-        }
-        if constexpr (TWO) {
-            // Quarter steps 4 s and 4 s + 2: the first group reads of stage s; 4 s + 1 and 4 s + 3: the
-            // second.  X and the scales of stage s are read by quarter 4 s + 1, the codes of the first
-            // parts by 4 s + 1, of the second by 4 s + 3.  Stage s + 2 takes their place:
-            //   codes: copies 0 .. 3 and the scales' in quarter 4 s + 3, 4 .. 7 in 4 s + 5 (with the reads
-            //   4 s + 2 and 4 s + 4); read from 4 s + 8 and 4 s + 10 on, so all but a wave's last 9 have
-            //   landed when it waits, after its instructions;
-            //   X: copies 0 .. 3 and the scales' in 4 s + 2, 4 .. 7 in 4 s + 4 (with the reads all in 4 s + 3);
-            //   read from 4 s + 8 on: the wait, in the reads of 4 s + 7, leaves 5 (ahead of the copies: 0).
-            static_assert(!TWO || (L == 8 && KG == 1 && BO == 256 && BT == 256), "two stages");
-            if (nk > 1) {
-                if (grp == 0) f8_wait_vm<5>();
-                else f8_wait_vm<9>();
-            } else {
+        f8_barrier();
+        int it = 0;
+        if (grp == 0) {
+            for (; it + 2 < nfull; ++it) {
+                if constexpr (INSIDE) step(First{}, it, none, spread(it + 1, 5, 9));
+                else step(First{}, it, [&] { together(it + 1, 5, 9); }, none);
+                f8_wait_vm<9>();
+                f8_barrier();
+                if constexpr (INSIDE) step(Second{}, it, none, spread(it + 2, 0, 5));
+                else step(Second{}, it, [&] { together(it + 2, 0, 5); }, none);
+                f8_wait_vm<9>();
+                f8_barrier();
+            }
+            for (; it < nk; ++it) {
+                step(First{}, it, [&] { copy_some(it + 1, 5, 9); }, none);
                 f8_wait_vm<0>();
+                f8_barrier();
+                step(Second{}, it, [&] { copy_some(it + 2, 0, 5); }, none);
+                f8_wait_vm<0>();
+                f8_barrier();
             }
             f8_barrier();
-            int it = 0;
-            if (grp == 0) {
-                for (; it + 2 < nfull; ++it) {
-                    if constexpr (INSIDE) step(First{}, it, none, spread(it + 1, 5, 9));
-                    else step(First{}, it, [&] { together(it + 1, 5, 9); }, none);
-                    f8_wait_vm<9>();
-                    f8_barrier();
-                    if constexpr (INSIDE) step(Second{}, it, none, spread(it + 2, 0, 5));
-                    else step(Second{}, it, [&] { together(it + 2, 0, 5); }, none);
-                    f8_wait_vm<9>();
-                    f8_barrier();
-                }
-                for (; it < nk; ++it) {
-                    step(First{}, it, [&] { copy_some(it + 1, 5, 9); }, none);
-                    f8_wait_vm<0>();
-                    f8_barrier();
-                    step(Second{}, it, [&] { copy_some(it + 2, 0, 5); }, none);
-                    f8_wait_vm<0>();
-                    f8_barrier();
-                }
-                f8_barrier();
-            } else {
-                f8_barrier();
-                for (; it + 2 < nfull; ++it) {
-                    if constexpr (INSIDE) step(First{}, it, none, spread(it + 2, 0, 5));
-                    else step(First{}, it, none, none);
-                    f8_barrier();
-                    if constexpr (INSIDE) step(Second{}, it, [] { f8_wait_vm<5>(); }, spread(it + 2, 5, 9));
-                    else step(Second{}, it, [&] { f8_wait_vm<0>(); together(it + 2, 0, 9); }, none);
-                    f8_barrier();
-                }
-                for (; it < nk; ++it) {
-                    step(First{}, it, none, none);
-                    f8_barrier();
-                    step(Second{}, it, [&] { f8_wait_vm<0>(); copy_some(it + 2, 0, 9); }, none);
-                    f8_barrier();
-                }
-            }
         } else {
-            // KG = 1: half steps 2 s (the first group reads stage s) and 2 s + 1 (the second does).  Under
-            // its matrix instructions of stage s the first group copies stage s + NST - 1, in the place of
-            // s - 1, the second s + NST, in the place of s; with the reads both copy s + NST - 1.  Stage s + 1
-            // has landed before half step 2 s + 2: the first group waits at the end of 2 s + 1 (with the
-            // reads: of 2 s), the second in its reads of stage s: NST - 2 stages may be in flight.
-            // KG = 2: a group's own stages; under its instructions of stage s it copies s + NST and waits
-            // after them.
-            constexpr int FLY = (L + 1) * (KG == 2 && INSIDE ? NST - 1 : NST - 2);
-            auto loop = [&](auto second) {
-                constexpr bool G1 = decltype(second)::value && KG == 1;
-                constexpr int DIST = INSIDE && (G1 || KG == 2) ? NST : NST - 1;
-                int it = 0;
-                for (; it + DIST < nfull; ++it) {
-                    if constexpr (INSIDE) {
-                        step(First{}, it, [] { if (G1) f8_wait_vm<FLY>(); }, spread(it + DIST, 0, L + 1));
-                        if (!G1) f8_wait_vm<FLY>();
-                    } else {
-                        step(First{}, it, [&] { together(it + DIST, 0, L + 1); f8_wait_vm<FLY>(); }, none);
-                    }
-                    f8_barrier();
-                }
-                for (; it < nk; ++it) {
-                    if constexpr (INSIDE) {
-                        step(First{}, it, [] { if (G1) f8_wait_vm<0>(); }, spread_some(it + DIST, 0, L + 1));
-                        if (!G1) f8_wait_vm<0>();
-                    } else {
-                        step(First{}, it, [&] { copy_some(it + DIST, 0, L + 1); f8_wait_vm<0>(); }, none);
-                    }
-                    f8_barrier();
-                }
-            };
-            if (nk < NST) f8_wait_vm<0>();                    // stage 0 has landed
-            else if (INSIDE && (KG == 2 || grp == 1)) f8_wait_vm<(L + 1) * (NST - 1)>();
-            else f8_wait_vm<(L + 1) * (NST - 2)>();
             f8_barrier();
-            if (KG == 2) {
-                if (grp == 1) f8_barrier();
-                loop(No{});
-            } else if (grp == 0) {
-                loop(No{});
-            } else {
-                f8_barrier();                                 // the second group runs half a step behind
-                loop(Yes{});
-            }
-            if (KG == 2 && nk < nmax) {                       // the other group's last stage
+            for (; it + 2 < nfull; ++it) {
+                if constexpr (INSIDE) step(First{}, it, none, spread(it + 2, 0, 5));
+                else step(First{}, it, none, none);
                 f8_barrier();
+                if constexpr (INSIDE) step(Second{}, it, [] { f8_wait_vm<5>(); }, spread(it + 2, 5, 9));
+                else step(Second{}, it, [&] { f8_wait_vm<0>(); together(it + 2, 0, 9); }, none);
                 f8_barrier();
             }
-            if (grp == 0) f8_barrier();                       // every wave has read its last stage
+            for (; it < nk; ++it) {
+                step(First{}, it, none, none);
+                f8_barrier();
+                step(Second{}, it, [&] { f8_wait_vm<0>(); copy_some(it + 2, 0, 9); }, none);
+                f8_barrier();
+            }
         }
-        rest(0);
+    } else {
+        // KG = 1: half steps 2 s (the first group reads stage s) and 2 s + 1 (the second does).  Under
+        // its matrix instructions of stage s the first group copies stage s + NST - 1, in the place of
+        // s - 1, the second s + NST, in the place of s; with the reads both copy s + NST - 1.  Stage s + 1
+        // has landed before half step 2 s + 2: the first group waits at the end of 2 s + 1 (with the
+        // reads: of 2 s), the second in its reads of stage s: NST - 2 stages may be in flight.
+        // KG = 2: a group's own stages; under its instructions of stage s it copies s + NST and waits
+        // after them.
+        constexpr int FLY = (L + 1) * (KG == 2 && INSIDE ? NST - 1 : NST - 2);
+        auto loop = [&](auto second) {
+            constexpr bool G1 = decltype(second)::value && KG == 1;
+            constexpr int DIST = INSIDE && (G1 || KG == 2) ? NST : NST - 1;
+            int it = 0;
+            for (; it + DIST < nfull; ++it) {
+                if constexpr (INSIDE) {
+                    step(First{}, it, [] { if (G1) f8_wait_vm<FLY>(); }, spread(it + DIST, 0, L + 1));
+                    if (!G1) f8_wait_vm<FLY>();
+                } else {
+                    step(First{}, it, [&] { together(it + DIST, 0, L + 1); f8_wait_vm<FLY>(); }, none);
+                }
+                f8_barrier();
+            }
+            for (; it < nk; ++it) {
+                if constexpr (INSIDE) {
+                    step(First{}, it, [] { if (G1) f8_wait_vm<0>(); }, spread_some(it + DIST, 0, L + 1));
+                    if (!G1) f8_wait_vm<0>();
+                } else {
+                    step(First{}, it, [&] { copy_some(it + DIST, 0, L + 1); f8_wait_vm<0>(); }, none);
+                }
+                f8_barrier();
+            }
+        };
+        if (nk < NST) f8_wait_vm<0>();                    // stage 0 has landed
+        else if (INSIDE && (KG == 2 || grp == 1)) f8_wait_vm<(L + 1) * (NST - 1)>();
+        else f8_wait_vm<(L + 1) * (NST - 2)>();
+        f8_barrier();
+        if (KG == 2) {
+            if (grp == 1) f8_barrier();
+            loop(No{});
+        } else if (grp == 0) {
+            loop(No{});
+        } else {
+            f8_barrier();                                 // the second group runs half a step behind
+            loop(Yes{});
+        }
+        if (KG == 2 && nk < nmax) {                       // the other group's last stage
+            f8_barrier();
+            f8_barrier();
+        }
+        if (grp == 0) f8_barrier();                       // every wave has read its last stage
+    }
+    rest(0);
 
-        // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
-        // second; each takes the other's sums of its half from LDS
-        constexpr int FH = KG == 2 ? FO / 2 : FO;
-        if constexpr (KG == 2) {
-            f32x4* x = (f32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
+    // KG = 2: group 0 finishes the first half of the wave's FO rows of fragments, group 1 the
+    // second; each takes the other's sums of its half from LDS
+    constexpr int FH = KG == 2 ? FO / 2 : FO;
+    if constexpr (KG == 2) {
+        f32x4* x = (f32x4*)smem + lane;                   // [group][wave][FH x FT][lane]
 #pragma unroll
-            for (int i = 0; i < FH; ++i)
+        for (int i = 0; i < FH; ++i)
 #pragma unroll
-                for (int j = 0; j < FT; ++j) {
-                    const f32x4 lo = acc[i][j], hi = acc[FH + i][j];
-                    f32x4 send, keep;
+            for (int j = 0; j < FT; ++j) {
+                const f32x4 lo = acc[i][j], hi = acc[FH + i][j];
+                f32x4 send, keep;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        send[e] = grp == 0 ? hi[e] : lo[e];
-                        keep[e] = grp == 0 ? lo[e] : hi[e];
-                    }
-                    x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
-                    acc[i][j] = keep;
+                for (int e = 0; e < 4; ++e) {
+                    send[e] = grp == 0 ? hi[e] : lo[e];
+                    keep[e] = grp == 0 ? lo[e] : hi[e];
                 }
-            f8_wait_lds();
-            f8_barrier();
-#pragma unroll
-            for (int i = 0; i < FH; ++i)
-#pragma unroll
-                for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
-        }
-        const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0), tb = at.t0 + wt * (BT / WT) + r;
-        const int64_t tend = at.end;
-        bool bad[FT];
-#pragma unroll
-        for (int j = 0; j < FT; ++j) bad[j] = tb + 16 * j < tend && f8_bad(a, tb + 16 * j);
-        // The next tile's first copies fly while this one's outputs are converted and stored
-        bool more = false;
-        if (PERSIST) {
-            tile += gridDim.x;
-            more = next();
-        }
-        bool stored = false;
-        if constexpr (FH % 2 == 0) {
-            if (a.splits == 1 && a.y_dtype != 0) {
-                stored = true;
-#pragma unroll
-                for (int j = 0; j < FT; ++j)
-#pragma unroll
-                    for (int i = 0; i < FH; i += 2)
-                        f8_put_pair16(a, acc[i][j], acc[i + 1][j], tb + 16 * j, tend, ob + 16 * i, c, bad[j]);
+                x[(((1 - grp) * 4 + wave) * (FH * FT) + i * FT + j) * 64] = send;
+                acc[i][j] = keep;
             }
-        }
-        if (!stored) {
+        f8_wait_lds();
+        f8_barrier();
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FT; ++j) acc[i][j] += x[((grp * 4 + wave) * (FH * FT) + i * FT + j) * 64];
+    }
+    const int64_t ob = o0 + wo * (BO / WO) + (KG == 2 ? grp * (FH * 16) : 0), tb = at.t0 + wt * (BT / WT) + r;
+    const int64_t tend = at.end;
+    bool bad[FT];
+#pragma unroll
+    for (int j = 0; j < FT; ++j) bad[j] = tb + 16 * j < tend && f8_bad(a, tb + 16 * j);
+    bool stored = false;
+    if constexpr (FH % 2 == 0) {
+        if (a.splits == 1 && a.y_dtype != 0) {
+            stored = true;
 #pragma unroll
             for (int j = 0; j < FT; ++j)
 #pragma unroll
-                for (int i = 0; i < FH; ++i) f8_out4(a, acc[i][j], tb + 16 * j, tend, ob + 16 * i + 4 * c, bad[j]);
+                for (int i = 0; i < FH; i += 2)
+                    f8_put_pair16(a, acc[i][j], acc[i + 1][j], tb + 16 * j, tend, ob + 16 * i, c, bad[j]);
         }
-        if (!more) break;
+    }
+    if (!stored) {
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < FH; ++i) f8_out4(a, acc[i][j], tb + 16 * j, tend, ob + 16 * i + 4 * c, bad[j]);
     }
 }
 
@@ -1108,8 +1091,7 @@ template <int BO, int BT, int NST, int WO, int KG, bool EXACT>
 hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
     a.tiles_m = (int)cdiv(a.m, BO);
     a.tiles_t = (int)f8_tiles_most(a.T, a.experts, BT);
-    const int64_t tiles = a.tiles_m * (int64_t)a.tiles_t;
-    const dim3 grid((unsigned)(f8_persist<BO, BT, KG> && tiles > F8_CUS ? F8_CUS : tiles), (unsigned)a.splits);
+    const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
     if (e8) hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, true, EXACT>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, false, EXACT>), grid, dim3(512), 0, s, a);
     return hipGetLastError();
@@ -1139,7 +1121,7 @@ hipError_t f8_run(F8Args a, bool e8, bool exact, const F8Plan& p, hipStream_t s)
     hipError_t e;
     switch (p.kind) {
         case 0: e = f8_tile_go<256, 256, 2, 2, 1, false>(a, e8, s); break;
-        case 1: e = f8_tile_go<256, 128, 3, 4, 1, false>(a, e8, s); break;
+        case 1: e = exact ? f8_tile_go<256, 128, 3, 4, 1, true>(a, e8, s) : f8_tile_go<256, 128, 3, 4, 1, false>(a, e8, s); break;
         case 2: e = exact ? f8_tile_go<128, 128, 4, 2, 1, true>(a, e8, s) : f8_tile_go<128, 128, 4, 2, 1, false>(a, e8, s); break;
         case 3: e = exact ? f8_tile_go<128, 64, 4, 4, 1, true>(a, e8, s) : f8_tile_go<128, 64, 4, 4, 1, false>(a, e8, s); break;
         case 4: e = exact ? f8_tile_go<64, 64, 4, 2, 2, true>(a, e8, s) : f8_tile_go<64, 64, 4, 2, 2, false>(a, e8, s); break;

@@ -104,8 +104,8 @@ struct F8TileCost {
 };
 constexpr F8TileCost f8_tiles[] = {
     {256, 256, 9.2f, 1.29f, 0.f},          // no float16 form: its fragments do not fit the registers
-    {256, 128, 7.3f, 0.88f, 0.f},
-    {128, 128, 6.25f, 0.527f, 0.945f},
+    {256, 128, 7.3f, 0.88f, 1.57f},
+    {128, 128, 6.25f, 0.527f, 0.915f},
     {128, 64, 5.65f, 0.385f, 0.624f},
     {64, 64, 5.2f, 0.227f, 0.345f},
 };

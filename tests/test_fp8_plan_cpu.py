@@ -26,7 +26,7 @@ int main() {
 }
 """
 ROW1, ROW2, TILES, ANY = -1, -2, 5, (8, 9, 10)
-NO_FLOAT16 = (0, 1)                       # tiles without a form for float32 outputs
+NO_FLOAT16 = (0,)                         # tiles without a form for float32 outputs
 
 
 @pytest.fixture(scope="module")
