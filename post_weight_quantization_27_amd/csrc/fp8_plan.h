@@ -103,11 +103,11 @@ struct F8TileCost {
     float fixed, step, step_exact; // us
 };
 constexpr F8TileCost f8_tiles[] = {
-    {256, 256, 9.2f, 1.29f, 0.f},          // no float16 form: its fragments do not fit the registers
-    {256, 128, 7.3f, 0.88f, 1.57f},
-    {128, 128, 6.25f, 0.527f, 0.915f},
-    {128, 64, 5.65f, 0.385f, 0.624f},
-    {64, 64, 5.2f, 0.227f, 0.345f},
+    {256, 256, 8.4f, 1.29f, 0.f},          // no float16 form: its fragments do not fit the registers
+    {256, 128, 6.15f, 0.89f, 1.565f},
+    {128, 128, 5.25f, 0.565f, 0.926f},
+    {128, 64, 4.6f, 0.435f, 0.595f},
+    {64, 64, 4.8f, 0.256f, 0.316f},
 };
 constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 
@@ -115,13 +115,14 @@ constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 // a second launch joins, and no less than memory takes; or the row kernel, whose workgroups stream their 16
 // rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359
 // shapes (768 .. 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts, each output
-// and scale type): the choice takes 2.0 % longer than the fastest kernel in the geometric mean and 32 % at
-// the worst (192 rows by 768 x 768: 7.3 against 5.5 us); 128 x 128 tiles alone take 58 % longer in the
-// mean and up to 5.8 times as long.
+// and scale type): the choice takes 1.5 % longer than the fastest kernel in the geometric mean and 31 % at
+// the worst (16 rows of 64 experts by 2816 x 2048: 24.8 against 19.0 us), and over 70 drawn shapes with
+// float32 outputs 0.6 % and 12 %; 128 x 128 tiles alone take 58 % longer in the mean and up to 5.3 times as
+// long.
 inline F8Plan f8_plan_fast(const F8Shape& s) {
     const F8Shares e = f8_shares(s.T, s.experts);
     const double bytes = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6;      // MB
-    const double mem = bytes / 5.0 + 2.7;
+    const double mem = bytes / 5.66 + 4.76;
     F8Plan best{F8_ANY, 1, s.n};
     double least = 1e30;
     for (int i = 0; i < F8_TILES; ++i) {
@@ -135,17 +136,19 @@ inline F8Plan f8_plan_fast(const F8Shape& s) {
             if (sp > 1 && p.splits < sp) continue;
             const double groups = tiles * p.splits / 256.0;
             const double rounds = s.experts > 1 ? (groups > 0.7 ? groups + 0.3 : 1.0) : ceil(groups);
-            const double work = 0.7 + rounds * (c.fixed + step * (double)p.kper / 128.0);
+            const double work = 0.6 + rounds * (c.fixed + step * (double)p.kper / 128.0);
             double t = work > mem ? work + 0.05 * mem : mem + 0.05 * work;
-            if (p.splits > 1) t += 3.4 + 0.31 * (double)p.splits * s.T * s.m * 4e-6;
+            if (p.splits > 1) t += 3.4 + 0.335 * (double)p.splits * s.T * s.m * 4e-6;
             if (t < least) { least = t; best = p; }
         }
     }
     if (e.rows <= 256.0 && f8_tiles_most(s.T, s.experts, 16) <= 65535) {
         const double groups = (double)f8_cdiv(s.m, 16) * f8_tiles_about(e, s.T, s.experts, 16, 8.0) / 256.0;
-        const double one = 1e-3 * (double)s.n * (1.0 + 0.335 * (e.rows < 16.0 ? e.rows : 16.0) / 16.0) * (groups > 1.0 ? groups : 1.0);
-        const double t1 = 3.2 + 0.74 * one + 0.695 * (double)f8_cdiv(s.n, 1024);
-        const double t2 = 3.2 + 0.909 * one + 0.255 * (double)f8_cdiv(s.n, 2048);
+        const double one = (1.0 + 0.31 * (e.rows < 16.0 ? e.rows : 16.0) / 16.0) * (groups > 1.0 ? groups : 1.0);
+        // turns of 512 and of 2048 k, a last one that is not full counted half
+        const int64_t turns1 = f8_cdiv(s.n, 512), turns2 = f8_cdiv(s.n, 2048);
+        const double t1 = 2.8 + 0.79e-3 * 0.5 * (double)(s.n + 512 * turns1) * one + 0.38 * (double)turns1;
+        const double t2 = 2.8 + 0.95e-3 * 0.5 * (double)(s.n + 2048 * turns2) * one + 0.17 * (double)turns2;
         if (t1 < least) { least = t1; best = f8_split(F8_ROW1, s.n, 1); }
         if (t2 < least) { least = t2; best = f8_split(F8_ROW2, s.n, 1); }
     }

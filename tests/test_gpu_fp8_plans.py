@@ -15,7 +15,7 @@ PRODUCTS = [  # rows, d_in, d_out, experts
     (1, 1040, 40, 1), (130, 1040, 1032, 1), (1300, 48, 6152, 1), (1300, 1040, 6152, 1), (400, 48, 8200, 1), (400, 1040, 8200, 1),
     (1600, 48, 1288, 1), (200, 1040, 8200, 1), (1300, 48, 776, 1), (65, 1040, 8200, 1), (257, 48, 40, 1), (257, 1040, 40, 1),
     (2060, 8208, 72, 1), (17, 6160, 4104, 1), (3, 8208, 40, 1), (17, 8208, 40, 1), (130, 20496, 2696, 1), (130, 16400, 5512, 1),
-    (1, 48, 40, 6), (1030, 400, 136, 6), (1300, 1040, 6152, 6), (65, 1040, 8200, 6), (1600, 48, 2056, 6), (2060, 1040, 776, 6),
+    (1, 48, 40, 6), (20, 4112, 40, 6), (1030, 400, 136, 6), (1300, 1040, 6152, 6), (65, 1040, 8200, 6), (1600, 48, 2056, 6), (2060, 1040, 776, 6),
     (520, 1040, 3100, 6), (2060, 48, 776, 6), (100, 1040, 3100, 6), (130, 1040, 3100, 6), (1600, 1040, 40, 6), (40, 8208, 40, 6),
     (65, 8208, 40, 6), (100, 6160, 776, 6), (130, 8208, 776, 6), (2060, 8208, 72, 6), (1030, 8208, 200, 6),
     (65, 400, 4104, 1), (65, 8208, 2056, 1), (400, 48, 6152, 6), (24, 1040, 8200, 6), (400, 48, 2696, 1), (1, 12304, 2056, 1), (700, 1040, 2056, 6),
@@ -27,9 +27,9 @@ PRODUCTS = [  # rows, d_in, d_out, experts
 
 # rows of any length that are copied to rows of 16-byte multiples first
 LAID = [
-    (2208, 131, 4037, 1), (371, 13409, 649, 1), (2031, 557, 1879, 1), (869, 139, 7308, 1), (1, 81505, 1, 1), (903, 4627, 521, 1),
-    (853, 2641, 1192, 1), (3174, 135, 2628, 6), (4872, 1431, 535, 6), (3779, 7455, 330, 6), (4344, 277, 1489, 6), (1, 82425, 1, 6),
-    (276, 3093, 1, 130), (385, 48235, 270, 1),
+    (2208, 131, 4037, 1), (2533, 129, 2294, 1), (2781, 16147, 129, 1), (3355, 399, 1035, 1), (845, 12929, 286, 1), (1170, 2203, 967, 1),
+    (419, 4095, 1157, 1), (262, 79215, 202, 1), (3174, 135, 2628, 6), (3738, 129, 1940, 6), (2019, 15035, 403, 6), (5521, 7953, 200, 6),
+    (2121, 8407, 521, 6), (3041, 3861, 483, 6), (2177, 8497, 273, 6), (276, 3093, 1, 130),
 ]
 
 
@@ -75,7 +75,12 @@ def test_kernels(pwq, T, n, m, E, out, scales):
         tol = (128 + G + 16) * 2.0 ** -23 * S + want.abs() * eps * 1.0001 + torch.finfo(dt).tiny * eps * 2
         if dt != torch.float32:
             tol += 2.0 ** -10 * S
-        off = (Y[a:b].double() - want).abs() - tol
+        y = Y[a:b].double()
+        off = (y - want).abs() - tol
+        if dt == torch.float16:
+            # 65504 + half a step of 32 = 65520 and everything beyond it rounds to infinity, so a value that
+            # the bar leaves on either side of 65520 may come out as one of its sign
+            off[(want.abs() + tol >= 65520) & (y == want.sign() * torch.inf)] = 0.0
         assert (off <= 0).all(), off.max()
         some = np.unique(np.concatenate([[a, b - 1], rng.integers(a, b, 6)]))
         cols = np.unique(np.concatenate([[0, m - 1], rng.integers(0, m, 30)]))
