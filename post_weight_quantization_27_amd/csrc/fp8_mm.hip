@@ -266,7 +266,8 @@ __device__ __forceinline__ int f8_pos(int r, int c) { return c ^ ((r >> 1) & 7);
 // any byte and have any length.  Operands travel through registers into LDS, two steps ahead; LDS
 // has two buffers and a step one barrier.  The last step may be partial: each 16 bytes past the end
 // is the row's last 16 instead, moved down in registers, with 0 behind in both operands (a byte
-// from elsewhere may be NaN).
+// from elsewhere may be NaN).  Loads at odd addresses bound it: 2000 rows by 8191 x d_in, bfloat16, 359 us
+// with d_in 8191, 280 with 8196 and 238 with 8192, and the tiles below 117.
 
 // The 16 bytes from byte `by` (0 .. 16) on, with 0 behind them
 __device__ __forceinline__ uint4 f8_drop(uint4 v, int by) {
@@ -463,13 +464,16 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
 // stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that the fragments
 // fit the registers, and each part of a stage is copied over as soon as it has been read (see the loop).
 //
-// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1460-1560 us with
-// float32 scales (2.5-2.6 PFLOP/s), 1310-1390 with powers of two (2.8-2.9), where the library's product
-// with one scale per tensor takes 1200-1330 on the same boards.  The clock falls to 1.75-2.0 GHz; a step of
-// 256 x 256 takes 2340 cycles with powers of two and about 3000 with float32 scales, of 2048 that its
-// instructions need.  One workgroup per compute unit going through its tiles loses with these (its next
-// tile's addresses spill: 8192^3 5 %, 2048 by 8192 x 8192 with powers of two 96 -> 107 us), as does leaving
-// out the instructions of waves without tokens (1460 -> 1560).
+// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1410-1550 us with
+// float32 scales (2.5-2.7 PFLOP/s), 1290-1350 with powers of two (2.85-2.98), where the library's product
+// with one scale per tensor takes 1200-1330 on the same boards; float32 outputs 8192^3 862 us (1.27
+// PFLOP/s on the float16 instructions, whose library product reaches 1.48).  The clock falls to 1.75-2.0
+// GHz; a step of 256 x 256 takes 2340 cycles with powers of two and about 3000 with float32 scales, of 2048
+// that its instructions need.  Of a tile's time 1.7 us go before its first copy, 1.4 to 2 until that has
+// landed and 3 to 4 into the outputs (32 steps of 4096 inputs: 45).  Workgroups that go through several
+// tiles lose: the next tile's addresses cost registers (256 x 256 spills, 8192^3 5 %; 128 x 128, 300 rows
+// by 50304 x 768 45 us in place of 40), as does leaving out the instructions of waves without tokens
+// (1460 -> 1560).
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 __device__ const uint4 f8_zeros = {0u, 0u, 0u, 0u};
@@ -936,7 +940,9 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
 // fragments (16 bytes of one row) straight into registers, those of a turn while the turn before is
 // multiplied, and the waves' sums meet in LDS.  No staging: a code is used once, and X comes from L2.
 // The float16 instructions cost nothing here.  Loads past the rows or tokens take a 16-byte block of
-// zeros as their address, so none waits behind a branch.
+// zeros as their address, so none waits behind a branch.  1 row by 8192 x 8192 17 us (4.0 TB/s), by 768 x
+// 768 3.8 (an empty launch takes 2.2).  Rows of any alignment lose this way: 1 row by 28671 x 8191 108 us,
+// 57 with the 64 x 32 tiles above.
 template <int U, int W, bool E8>
 __global__ __launch_bounds__(64 * W) void f8_row_kernel(F8Args a) {
     __shared__ f32x4 red[W][64];
@@ -1022,7 +1028,8 @@ __global__ __launch_bounds__(64 * W) void f8_row_kernel(F8Args a) {
 }
 
 // ------------------------------------------------------------------ splits
-// The splits' sums of four outputs of a row at a time, in their order.  grid: x = outputs, y = rows
+// The splits' sums of four outputs of a row at a time, in their order: a launch's latency, 4.5 us behind
+// the tiles.  grid: x = outputs, y = rows
 __global__ __launch_bounds__(256) void f8_join_kernel(F8Args a) {
     const int64_t o = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (o >= a.m) return;

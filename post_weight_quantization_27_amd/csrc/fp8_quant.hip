@@ -189,7 +189,8 @@ __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
 }
 
 // ------------------------------------------------------------------ weights
-// A workgroup holds a block of 128 x 128, 64 values a thread.
+// A workgroup holds a block of 128 x 128, 64 values a thread.  Memory bounds it: 8192 x 28672 float16 141
+// us (5.0 TB/s), float32 217 (5.4); rows of odd length 8191 x 8191 bfloat16 58, where 8192 x 8192 takes 45.
 template <int XT, int AL, bool E8>
 __global__ __launch_bounds__(256) void f8_blocks_kernel(F8QuantArgs a) {
     __shared__ float slot[2][4];
