@@ -115,9 +115,9 @@ constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 // a second launch joins, and no less than memory takes; or the row kernel, whose workgroups stream their 16
 // rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359
 // shapes (768 .. 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts, each output
-// and scale type): the choice takes 1.4 % longer than the fastest kernel in the geometric mean and 28 % at
-// the worst (4096 rows of 8 experts by 2048 x 4096: 66.6 against 52.2 us), and over 70 drawn shapes with
-// float32 outputs 0.9 % and 24 %; 128 x 128 tiles alone take 58 % longer in the mean and up to 5.3 times as
+// and scale type): the choice takes 1.3 % longer than the fastest kernel in the geometric mean and 26 % at
+// the worst (256 rows of 8 experts by 2048 x 4096: 27.3 against 21.7 us), and over 70 drawn shapes with
+// float32 outputs 1.1 % and 24 %; 128 x 128 tiles alone take 58 % longer in the mean and up to 5.3 times as
 // long.
 inline F8Plan f8_plan_fast(const F8Shape& s) {
     const F8Shares e = f8_shares(s.T, s.experts);
@@ -135,7 +135,7 @@ inline F8Plan f8_plan_fast(const F8Shape& s) {
             const F8Plan p = f8_split(i, s.n, sp);
             if (sp > 1 && p.splits < sp) continue;
             const double groups = tiles * p.splits / 256.0;
-            const double rounds = s.experts > 1 ? (groups > 0.7 ? groups + 0.3 : 1.0) : ceil(groups);
+            const double rounds = s.experts > 1 ? (groups > 0.6 ? groups + 0.4 : 1.0) : ceil(groups);
             const double work = 0.6 + rounds * (c.fixed + step * (double)p.kper / 128.0);
             double t = work > mem ? work + 0.1 * mem : mem + 0.1 * work;
             if (p.splits > 1) t += 3.4 + 0.335 * (double)p.splits * s.T * s.m * 4e-6;

@@ -28,9 +28,8 @@ PRODUCTS = [  # rows, d_in, d_out, experts
 # rows of any length that are copied to rows of 16-byte multiples first
 LAID = [
     (2208, 131, 4037, 1), (2533, 129, 2294, 1), (2781, 16147, 129, 1), (2358, 583, 1290, 1), (371, 13409, 649, 1), (1295, 2503, 835, 1),
-    (1456, 4733, 343, 1), (262, 79215, 202, 1), (3174, 135, 2628, 6), (3738, 129, 1940, 6), (2019, 15035, 403, 6), (2056, 12767, 415, 6),
-    (2121, 8407, 521, 6), (3898, 5249, 360, 6), (2177, 8497, 273, 6), (276, 3093, 1, 130), (4000, 1601, 2003, 1), (5000, 4111, 1003, 6),
-    (2422, 30267, 264, 6),
+    (1456, 4733, 343, 1), (262, 79215, 202, 1), (4000, 1601, 2003, 1), (3174, 135, 2628, 6), (4000, 129, 2600, 6), (2019, 15035, 403, 6),
+    (3167, 9261, 449, 6), (5648, 1807, 516, 6), (3400, 11027, 268, 6), (5000, 4111, 1003, 6), (2422, 30267, 264, 6), (276, 3093, 1, 130),
 ]
 
 
