@@ -85,6 +85,11 @@ listed in the design notes):
 * G1  The product with the quantized weights ([GPTQ-P] "Running GPTQ with AutoGPTQ": the
       quantized model runs inference on them) is Y = X What^T, What decoded exactly as in
       ``dequant``; tokens x d_in times d_out x d_in gives tokens x d_out.
+* F1  8-bit floating point ([MQM] section 1 with Z = 0; the pages name no float format): OCP
+      e4m3 codes (largest 448) of blocks of 128 x 128 weights or 128 values of a token.
+      s = fp32(top / 448), below 2^-120 taken as 0; or the least 2^n, n >= -127, with top <=
+      448 2^n.  Code = the e4m3 value nearest to the exact quotient, ties to even; s = 0 gives
+      code 0, a value that is not finite gives s = NaN and codes 0.
 
 Pins (tests/test_oracle_pins.py):
   rtn / quantize_codes / group_scales : golden tie-to-even rows, code range, error bound,
@@ -117,6 +122,9 @@ Pins (tests/test_oracle_pins.py):
   tensor_scales                       : the per-row rule on the flattened matrix; the
                                         tensor's absmax element maps to +-qmax; GPTQ with a
                                         diagonal H and these scales equals RTN with them
+  e4m3_values / quantize_*_fp8 / quantized_matmul_fp8* : (tests/test_fp8_cpu.py) the format's
+                                        table, ties, borders, zeros and non-finite blocks;
+                                        products against sums written out
 """
 from __future__ import annotations
 
