@@ -464,8 +464,8 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
 // stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that the fragments
 // fit the registers, and each part of a stage is copied over as soon as it has been read (see the loop).
 //
-// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1410-1550 us with
-// float32 scales (2.5-2.7 PFLOP/s), 1290-1350 with powers of two (2.85-2.98), where the library's product
+// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1410-1580 us with
+// float32 scales (2.4-2.7 PFLOP/s), 1290-1375 with powers of two (2.8-2.98), where the library's product
 // with one scale per tensor takes 1200-1330 on the same boards; float32 outputs 8192^3 862 us (1.27
 // PFLOP/s on the float16 instructions, whose library product reaches 1.48).  The clock falls to 1.75-2.0
 // GHz; a step of 256 x 256 takes 2340 cycles with powers of two and about 3000 with float32 scales, of 2048
@@ -490,8 +490,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t f8_buffer(const uint8_t* base)
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, -1, 0x00027000);
 }
 
+template <int BO, int BT, int NST, int KG>
+constexpr int f8_smem = KG * NST * ((BO + BT) * F8_B + 8 / KG * 256);
+
 template <int BO, int BT, int NST, int WO, int KG, bool E8, bool EXACT>
-__global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
+__device__ __forceinline__ void f8_tile_body(const F8Args& a, uint8_t* smem, int to, const F8Rows& at) {
     constexpr int BK = F8_B, NW = 8 / KG, WT = NW / WO;   // waves that share a stage
     constexpr int FO = BO / WO / 16, FT = BT / WT / 16;
     constexpr int FP = NST == 2 ? FO / 2 : FO;            // rows of fragments in registers at a time
@@ -503,7 +506,7 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     static_assert(L * NW * 8 == BO + BT && BO % (NW * 8) == 0 && (L + 1) * (NST - 1) < 64 && KG * NST * ST <= 163840, "tile");
     static_assert(BO / WO <= F8_B && BT % 64 == 0 && BT / 64 < NW, "scales");
     static_assert(KG == 1 || (NST > 2 && FO % 2 == 0 && 8 * FO / 2 * FT * 1024 <= 2 * NST * ST), "the groups' sums fit the stages");
-    __shared__ __attribute__((aligned(16))) uint8_t smem[KG * NST * ST];
+    static_assert(KG * NST * ST == f8_smem<BO, BT, NST, KG>, "stages");
     const int lane = threadIdx.x & 63, wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = KG == 2 ? wave8 & 3 : wave8, grp = wave8 >> 2;
     const int wo = wave / WT, wt = wave % WT;
@@ -537,45 +540,37 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     const uint8_t* sbase;
     int64_t sstep;
     uint32_t off[L];
-    F8Rows at;
-    int64_t o0;
+    const int64_t o0 = (int64_t)to * BO;
     // The order of k is free, so tiles that live on the codes' traffic start at different k: where d_in
     // is a multiple of 4096, rows that are read at the same k in step all come from the same few
     // memory channels.  Large token tiles share X by k instead and start together.
     constexpr int ROT = BT <= 128 ? 3 : 0;
-    int rot;
-    auto setup = [&](uint32_t tile) {
-        int to;
-        if (!f8_tile<BT>(a, tile, to, at)) return false;
-        o0 = (int64_t)to * BO;
-        rot = ROT && nfull > 0 ? (int)((uint32_t)(to * ROT) % (uint32_t)nfull) : 0;
-        cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
-        xbase = a.X + (a.rows && !a.laid ? 0 : at.t0 * a.ldx) + kbeg;
-        cbuf = f8_buffer(TWO && grp == 1 ? xbase : cbase);
-        xbuf = f8_buffer(xbase);                          // two stages: a wave copies rows of one operand alone, cbuf's
+    const int rot = ROT && nfull > 0 ? (int)((uint32_t)(to * ROT) % (uint32_t)nfull) : 0;
+    cbase = a.C + ((int64_t)at.expert * a.m + o0) * a.n + kbeg;
+    xbase = a.X + (a.rows && !a.laid ? 0 : at.t0 * a.ldx) + kbeg;
+    cbuf = f8_buffer(TWO && grp == 1 ? xbase : cbase);
+    xbuf = f8_buffer(xbase);                          // two stages: a wave copies rows of one operand alone, cbuf's
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int r = row0(j) + (lane >> 3);
-            const int ch = f8_pos(r & 15, lane & 7);      // the xor undoes itself
-            if (of_x(j)) {
-                const int64_t t = at.t0 + r - BO < at.end ? at.t0 + r - BO : at.end - 1;
-                off[j] = (uint32_t)((a.rows && !a.laid ? f8_xrow(a, t) : t - at.t0) * a.ldx + 16 * ch);
-            } else {
-                off[j] = (uint32_t)((o0 + r < a.m ? r : a.m - 1 - o0) * a.n + 16 * ch);
-            }
-        }
-        constexpr int SB = E8 ? 1 : 4;
-        const int64_t b = kbeg / BK;
-        if (slot < BT / 64) {
-            const int64_t t = at.t0 + 64 * slot + lane < at.end ? at.t0 + 64 * slot + lane : at.end - 1;
-            sbase = (const uint8_t*)a.sx + (b * a.ldsx + f8_xrow(a, t)) * SB;
-            sstep = a.ldsx * SB;
+    for (int j = 0; j < L; ++j) {
+        const int r = row0(j) + (lane >> 3);
+        const int ch = f8_pos(r & 15, lane & 7);      // the xor undoes itself
+        if (of_x(j)) {
+            const int64_t t = at.t0 + r - BO < at.end ? at.t0 + r - BO : at.end - 1;
+            off[j] = (uint32_t)((a.rows && !a.laid ? f8_xrow(a, t) : t - at.t0) * a.ldx + 16 * ch);
         } else {
-            sbase = (const uint8_t*)a.sw + f8_sw_at(a, at.expert, o0 + F8_B * (lane % NB), b) * SB;
-            sstep = SB;
+            off[j] = (uint32_t)((o0 + r < a.m ? r : a.m - 1 - o0) * a.n + 16 * ch);
         }
-        return true;
-    };
+    }
+    constexpr int SB = E8 ? 1 : 4;
+    const int64_t b = kbeg / BK;
+    if (slot < BT / 64) {
+        const int64_t t = at.t0 + 64 * slot + lane < at.end ? at.t0 + 64 * slot + lane : at.end - 1;
+        sbase = (const uint8_t*)a.sx + (b * a.ldsx + f8_xrow(a, t)) * SB;
+        sstep = a.ldsx * SB;
+    } else {
+        sbase = (const uint8_t*)a.sw + f8_sw_at(a, at.expert, o0 + F8_B * (lane % NB), b) * SB;
+        sstep = SB;
+    }
     // copy j of stage `it` (j = L: the scales).  END: the last stage where it ends past the rows: zeros
     // there in both operands (a byte from elsewhere may be NaN)
     auto copy = [&](auto end, int it, int j) {
@@ -758,7 +753,6 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
         };
     };
     // the first stages
-    if (!setup(blockIdx.x)) return;
     if constexpr (TWO) {
         copy_some(0, 0, L + 1);
         copy_some(1, 0, grp == 0 ? 5 : L + 1);
@@ -934,6 +928,26 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     }
 }
 
+// HALF: a tile of 256 x 256 with no more than 128 rows, an expert's last, is one of 256 x 128 (16384 rows
+// of 64 experts by 4096 x 4096 396 -> 379 us, of 128 by 1024 x 2048 103 -> 90; 32768 of 64, at the power
+// limit, 622 -> 615).  One matrix has one such tile a column at most, and loses up to 1 % to it.
+template <int BO, int BT, int NST, int WO, int KG, bool E8, bool EXACT, bool HALF>
+__global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
+    static_assert(!HALF || (BO == 256 && BT == 256), "half a tile");
+    constexpr int MINE = f8_smem<BO, BT, NST, KG>, OTHER = HALF ? f8_smem<256, 128, 3, 1> : 0;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[MINE > OTHER ? MINE : OTHER];
+    int to;
+    F8Rows at{0, 0, 0};
+    if (!f8_tile<BT>(a, blockIdx.x, to, at)) return;
+    if constexpr (HALF) {
+        if (at.end - at.t0 <= 128) {
+            f8_tile_body<256, 128, 3, 4, 1, E8, EXACT>(a, smem, to, at);
+            return;
+        }
+    }
+    f8_tile_body<BO, BT, NST, WO, KG, E8, EXACT>(a, smem, to, at);
+}
+
 // ------------------------------------------------------------------ few tokens
 // Few tokens, where the weights are the traffic or a launch's latency counts: a workgroup owns 16
 // outputs by 16 tokens, its W waves share k in turns of U blocks each, every lane loads its
@@ -1094,13 +1108,13 @@ __global__ __launch_bounds__(256) void f8_lay_kernel(F8Args a, uint8_t* X, uint8
 }
 
 // ------------------------------------------------------------------ launches
-template <int BO, int BT, int NST, int WO, int KG, bool EXACT>
+template <int BO, int BT, int NST, int WO, int KG, bool EXACT, bool HALF = false>
 hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
     a.tiles_m = (int)cdiv(a.m, BO);
     a.tiles_t = (int)f8_tiles_most(a.T, a.experts, BT);
     const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_t), (unsigned)a.splits);
-    if (e8) hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, true, EXACT>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, false, EXACT>), grid, dim3(512), 0, s, a);
+    if (e8) hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, true, EXACT, HALF>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((f8_tile_kernel<BO, BT, NST, WO, KG, false, EXACT, HALF>), grid, dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1127,7 +1141,9 @@ hipError_t f8_run(F8Args a, bool e8, bool exact, const F8Plan& p, hipStream_t s)
     a.kper = p.kper;
     hipError_t e;
     switch (p.kind) {
-        case 0: e = f8_tile_go<256, 256, 2, 2, 1, false>(a, e8, s); break;
+        case 0:
+            e = a.offsets ? f8_tile_go<256, 256, 2, 2, 1, false, true>(a, e8, s) : f8_tile_go<256, 256, 2, 2, 1, false>(a, e8, s);
+            break;
         case 1: e = exact ? f8_tile_go<256, 128, 3, 4, 1, true>(a, e8, s) : f8_tile_go<256, 128, 3, 4, 1, false>(a, e8, s); break;
         case 2: e = exact ? f8_tile_go<128, 128, 4, 2, 1, true>(a, e8, s) : f8_tile_go<128, 128, 4, 2, 1, false>(a, e8, s); break;
         case 3: e = exact ? f8_tile_go<128, 64, 4, 4, 1, true>(a, e8, s) : f8_tile_go<128, 64, 4, 4, 1, false>(a, e8, s); break;
