@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define PWQ_ABI_VERSION 7
+#define PWQ_ABI_VERSION 8
 
 typedef enum pwq_status {
     PWQ_OK = 0,
@@ -535,15 +535,19 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *   X         n_tok x d_in e4m3 codes, leading dimension ldx; x_scales groups x n_tok, leading
  *             dimension lds; codes d_out x d_in, dense; scales (d_out / 128) x groups, dense: the
  *             formats above, both scales of scale_type.
- *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy.
+ *   Y         n_tok x d_out, y_dtype PWQ_F32 / PWQ_F16 / PWQ_BF16, leading dimension ldy; a 16-bit type
+ *             may have PWQ_E4M3_SUMS or'd to it (see below).
  *   ws        pwq_quantized_matmul_fp8_workspace_size(n_tok, d_in, d_out) bytes, 16-byte aligned (0
  *             bytes: ws may be NULL): the float32 sums of a split k and, where d_in is no multiple of
  *             16 and there are rows enough, copies of X and of the codes (about as many bytes as they).
- * A block's sum over k is multiplied by the product of its two scales, formed in float32, and added to a
- * float32 sum.  With float32 Y that sum over k is of exact products in float32.  With 16-bit Y it may come
- * from the e4m3 matrix instruction, which of each eight consecutive products keeps what is at least 2^-13
- * of the largest: off by less than 2^-10 of the largest of each eight (about 5e-5 of the result's norm on
- * normal data, a rounding to float16 2e-4).
+ * A block's sum over k, of exact products in float32, is multiplied by the product of its two scales,
+ * formed in float32, and added to a float32 sum, which is rounded once to Y's type.
+ * With PWQ_E4M3_SUMS the sums may come from the e4m3 matrix instruction, at up to twice the rate where there
+ * are a few hundred tokens or more.  Of each eight consecutive products it keeps what is at least 2^-13 of the
+ * largest: off by less than 2^-10 of the largest of each eight, with every scale multiplied in (1.5e-5 to 5e-5
+ * of the result's norm on normal data, where a rounding to float16 is 2e-4; all of a result that is small
+ * products beside large ones that cancel).  Scales that are powers of two then go into the instruction, which
+ * adds a block to the float32 sum itself.  PWQ_EDTYPE with PWQ_F32.
  * Any alignment and sizes; rows of X and codes that start at multiples of 16 bytes take the faster
  * kernels, as do the copies of rows of other lengths.  Codes of NaN and scales of NaN give NaN.
  *
@@ -556,10 +560,11 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *             the nearer end; offsets that decrease leave Y's rows undefined.
  *   rows      optional DEVICE int32[n_rows], 0 .. n_x - 1, one row as often as wanted.  Another index
  *             gives a row of NaN.
- *   Y         n_rows x d_out; rows before offsets[0] and from offsets[n_experts] on are left alone.
+ *   Y         n_rows x d_out, y_dtype as above; rows before offsets[0] and from offsets[n_experts] on are left alone.
  *   ws        pwq_quantized_matmul_fp8_grouped_workspace_size(n_rows, d_in, d_out, n_experts) bytes.
  * PWQ_EINVAL when Y needs more tiles of 64 x 64 than one launch holds (2^23).  Calls that may run at
  * the same time need a ws each. */
+#define PWQ_E4M3_SUMS 0x100
 size_t pwq_quantized_matmul_fp8_workspace_size(int64_t n_tok, int64_t d_in, int64_t d_out);
 pwq_status pwq_quantized_matmul_fp8(const uint8_t* X, int64_t n_tok, int64_t d_in, int64_t ldx, const void* x_scales,
                                     int64_t lds, int scale_type, const uint8_t* codes, const void* scales, int64_t d_out,

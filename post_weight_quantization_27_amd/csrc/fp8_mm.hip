@@ -7,13 +7,16 @@
 //
 // The matrix instruction on e4m3 operands (K = 128, a block at a time) does not hold its sum in 32
 // bits: of each eight consecutive products it keeps what is at least 2^-13 of the largest one's power
-// of two (measured: 2^16 + 2^2 gives 2^16).  Codes convert exactly to float16, whose products and sums
-// the float16 instruction holds in float32, at half the rate.  So
-//   EXACT   float32 outputs, and wherever the weights' traffic is the bound: float16 instructions
-//           (error against 64 bits 1.0e-7 of normal data's norm at 8192 inputs);
-//   !EXACT  16-bit outputs of tiles, whose own rounding (1.7e-3 of the norm in bfloat16, 2.1e-4 in
-//           float16) hides the e4m3 instruction's 1.5e-5 to 5e-5.
-// A block's sum is multiplied by its two scales and added to the output's float32 sum.
+// of two (measured: 2^16 + 2^2 gives 2^16), so large products that cancel can take a result with them.
+// Codes convert exactly to float16, whose products and sums the float16 instruction holds in float32, at
+// half the rate.  So
+//   EXACT   whatever the output's type: float16 instructions (error against 64 bits 1.0e-7 of normal
+//           data's norm at 8192 inputs).  The row kernel and the joins of splits have no other form;
+//   !EXACT  tiles whose 16-bit outputs the caller asks for with PWQ_E4M3_SUMS: the e4m3 instruction, off
+//           by 1.5e-5 to 5e-5 of normal data's norm, beside the output's own rounding (1.7e-3 in bfloat16,
+//           2.1e-4 in float16).
+// A block's sum is multiplied by its two scales and added to the output's float32 sum; powers of two with
+// !EXACT go into the instruction, which adds the block to the sum itself.
 #include "../../include/pwq.h"
 #include "fp8.h"
 #include "fp8_plan.h"
@@ -1173,7 +1176,7 @@ hipError_t f8_launch(const F8Call& c, hipStream_t s) {
     // 32-bit offsets: from a tile's first row, or from X's with rows
     const bool near = c.n < ((int64_t)1 << 24) && (c.rows ? c.xrows * c.ldx < ((int64_t)1 << 32) : c.ldx < ((int64_t)1 << 24));
     const bool fast = c.n % 16 == 0 && c.ldx % 16 == 0 && aligned(c.X, 16) && aligned(c.C, 16) && near;
-    const bool exact = c.y_dtype == 0;
+    const bool exact = !c.e4m3_sums;
     const F8Plan p = f8_plan(F8Shape{c.T, c.n, c.m, c.experts, exact, fast});
     if (p.lay) {
         uint8_t* const X = (uint8_t*)c.ws + f8_plan_ws_sums(p, c.T, c.m);

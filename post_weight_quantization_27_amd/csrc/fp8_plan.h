@@ -22,9 +22,9 @@ struct F8Plan {
 };
 constexpr int F8_ROW1 = -1, F8_ROW2 = -2, F8_ANY = 8;
 
-// What decides: rows of Y, d_in, d_out, experts (1: one matrix), whether the float16 instructions are
-// asked for (float32 outputs), whether operand rows start at multiples of 16 bytes and lie within
-// 32-bit offsets of a tile's base
+// What decides: rows of Y, d_in, d_out, experts (1: one matrix), whether the sums are the float16
+// instructions' (exact), whether operand rows start at multiples of 16 bytes and lie within 32-bit
+// offsets of a tile's base (fast)
 struct F8Shape {
     int64_t T, n, m, experts;
     bool exact, fast;
@@ -187,7 +187,7 @@ inline size_t f8_plan_ws_sums(const F8Plan& p, int64_t T, int64_t m) {
     return p.splits > 1 ? ((size_t)p.splits * (size_t)T * (size_t)m * sizeof(float) + 15) / 16 * 16 : 0;
 }
 inline size_t f8_plan_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts) {
-    // the outputs' type, and where rows start, are the call's affair: room for any of its plans
+    // whose sums, and where rows start, are the call's affair: room for any of its plans
     size_t most = 0;
     for (int i = 0; i < (n % 16 == 0 ? 4 : 2); ++i) {
         const F8Plan p = f8_plan(F8Shape{T, n, m, experts, (i & 1) != 0, (i & 2) != 0});

@@ -621,7 +621,9 @@ static size_t fp8_workspace(int64_t n_rows, int64_t d_in, int64_t d_out, int64_t
     return f8_ws_bytes(n_rows, d_in, d_out, n_experts);
 }
 static pwq_status fp8_matmul(F8Call c, int scale_type, size_t ws_bytes, void* stream) {
-    if (!float_dtype(c.y_dtype) || !scale_type_ok(scale_type)) return PWQ_EDTYPE;
+    c.e4m3_sums = (c.y_dtype & PWQ_E4M3_SUMS) != 0;
+    c.y_dtype &= ~PWQ_E4M3_SUMS;
+    if (!float_dtype(c.y_dtype) || (c.e4m3_sums && c.y_dtype == PWQ_F32) || !scale_type_ok(scale_type)) return PWQ_EDTYPE;
     if (!fp8_dims_ok(c.T, c.n, c.m, c.experts) || bad_dim(c.xrows) || c.ldx < c.n || bad_dim(c.ldx) || c.ldsx < c.xrows ||
         bad_dim(c.ldsx) || c.ldy < c.m || bad_dim(c.ldy))
         return PWQ_EINVAL;
@@ -652,7 +654,7 @@ pwq_status pwq_quantized_matmul_fp8(const uint8_t* X, int64_t n_tok, int64_t d_i
                                     int64_t lds, int scale_type, const uint8_t* codes, const void* scales, int64_t d_out,
                                     void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
     return fp8_matmul(F8Call{X, x_scales, codes, scales, nullptr, nullptr, Y, ws, n_tok, ldx, lds, ldy, n_tok, d_in, d_out, 1,
-                             y_dtype, false},
+                             y_dtype, false, false},
                       scale_type, ws_bytes, stream);
 }
 
@@ -667,7 +669,7 @@ pwq_status pwq_quantized_matmul_fp8_grouped(const uint8_t* X, int64_t n_x, int64
                                             void* stream) {
     if (n_rows > 0 && d_out > 0 && !offsets) return PWQ_EINVAL;
     return fp8_matmul(F8Call{X, x_scales, codes, scales, offsets, rows, Y, ws, n_x, ldx, lds, ldy, n_rows, d_in, d_out,
-                             n_experts, y_dtype, false},
+                             n_experts, y_dtype, false, false},
                       scale_type, ws_bytes, stream);
 }
 

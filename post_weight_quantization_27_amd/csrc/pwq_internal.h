@@ -120,7 +120,7 @@ struct F8Call {
     void* ws;
     int64_t xrows, ldx, ldsx, ldy, T, n, m, experts;       // X's rows; Y's rows, d_in, d_out
     int y_dtype;
-    bool e8;
+    bool e8, e4m3_sums;            // e4m3_sums: tiles' sums from the e4m3 instruction (16-bit Y)
 };
 bool f8_size_ok(int64_t T, int64_t m, int64_t experts);
 size_t f8_ws_bytes(int64_t T, int64_t n, int64_t m, int64_t experts);

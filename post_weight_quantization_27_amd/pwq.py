@@ -658,6 +658,7 @@ def quantized_matmul_int8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.
 
 # ------------------------------------------------------------------ 8-bit floating point
 _E4M3 = torch.float8_e4m3fn
+PWQ_E4M3_SUMS = 0x100
 _SCALES = {torch.float32: 0, torch.float8_e8m0fnu: 1}
 
 
@@ -772,11 +773,11 @@ def _fp8_operands(X, x_scales, codes, scales, dev, rank: int):
 
 def quantized_matmul_fp8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                          out_dtype=torch.float16, out: Optional[torch.Tensor] = None,
-                         ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                         ws: Optional[torch.Tensor] = None, e4m3_sums: bool = False) -> torch.Tensor:
     """Y = X What^T on e4m3 codes with a scale per block of 128: X, x_scales from quantize_tokens_fp8,
-    codes, scales from quantize_blocks_fp8 (both scales of one type).  float32 outputs are sums of exact
-    products in float32; 16-bit ones may go through the e4m3 matrix instruction, whose sums are off by up to
-    2^-10 of the largest product of each eight."""
+    codes, scales from quantize_blocks_fp8 (both scales of one type).  Outputs are float32 sums of exact
+    products, rounded once.  ``e4m3_sums`` (16-bit outputs): sums may be the e4m3 matrix instruction's, at
+    up to twice the rate for prompts, off by up to 2^-10 of the largest product of each eight."""
     dev = X.device
     ldx, lds, st, c, sw = _fp8_operands(X, x_scales, codes, scales, dev, 2)
     T, d = X.shape
@@ -788,13 +789,14 @@ def quantized_matmul_fp8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.T
     w, nb, ws = _fp8_ws(ws, dev, T, d, m, 1)
     _check("pwq_quantized_matmul_fp8", _on(
         X, lib().pwq_quantized_matmul_fp8, X.data_ptr(), T, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, out.data_ptr(),
-        _CODES.get(out.dtype, -1), ldy, w, nb))
+        _CODES.get(out.dtype, -1) | (PWQ_E4M3_SUMS if e4m3_sums else 0), ldy, w, nb))
     return out
 
 
 def quantized_matmul_fp8_grouped(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
                                  offsets: torch.Tensor, rows: Optional[torch.Tensor] = None, out_dtype=torch.float16,
-                                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                                 out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                                 e4m3_sums: bool = False) -> torch.Tensor:
     """quantized_matmul_fp8 with one of several weight matrices for each row: codes (experts x d_out x
     d_in) and scales from quantize_blocks_fp8 of the stack.  Output rows offsets[e] .. offsets[e + 1] - 1
     (int32 on the GPU, experts + 1 of them, not decreasing) multiply expert e's.  ``rows`` (int32 on the
@@ -818,7 +820,7 @@ def quantized_matmul_fp8_grouped(X: torch.Tensor, x_scales: torch.Tensor, codes:
     w, nb, ws = _fp8_ws(ws, dev, T, d, m, E)
     _check("pwq_quantized_matmul_fp8_grouped", _on(
         X, lib().pwq_quantized_matmul_fp8_grouped, X.data_ptr(), n_x, d, ldx, x_scales.data_ptr(), lds, st, c, sw, m, E, off,
-        r, T, out.data_ptr(), _CODES.get(out.dtype, -1), ldy, w, nb))
+        r, T, out.data_ptr(), _CODES.get(out.dtype, -1) | (PWQ_E4M3_SUMS if e4m3_sums else 0), ldy, w, nb))
     return out
 
 
