@@ -46,7 +46,7 @@ struct F8Args {
     int64_t T, n, m;               // output rows, d_in, d_out
     int64_t xrows, kper;           // X's rows; k per split
     int experts, groups, splits, y_dtype;
-    int tiles_t, tiles_m;
+    int tiles_t, tiles_m;          // launched
     bool laid;                     // X is a copy, a row for each output row
 };
 
@@ -58,7 +58,8 @@ struct F8Rows {
 
 // The experts' rows are cut into tiles of BT, one expert after the other.  Every wave counts them through
 // the offsets, 64 experts at a time.  Offsets are taken into 0 .. T, and a tile has to start inside its
-// expert's rows, so whatever the offsets hold no row outside Y is touched.
+// expert's rows, and no more tiles count than were launched, so whatever the offsets hold no row outside Y is
+// touched and no output outside 0 .. d_out - 1.
 template <int BT>
 struct F8Count {
     int64_t lo, hi;                // of this lane's expert
@@ -67,12 +68,10 @@ struct F8Count {
         const int lane = threadIdx.x & 63;
         lo = hi = 0;
         if (e0 + lane < a.experts) {
-            lo = a.offsets[e0 + lane];
-            hi = a.offsets[e0 + lane + 1];
-            lo = lo < 0 ? 0 : lo;
-            hi = hi > a.T ? a.T : hi;
+            lo = f8_low(a.offsets[e0 + lane]);
+            hi = f8_high(a.offsets[e0 + lane + 1], a.T);
         }
-        own = hi > lo ? (int)((hi - lo + BT - 1) / BT) : 0;
+        own = f8_own(lo, hi, BT, a.tiles_t);
         upto = own;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -118,28 +117,22 @@ __device__ __forceinline__ bool f8_bad(const F8Args& a, int64_t t) {
     return a.rows && (uint32_t)a.rows[t] >= (uint64_t)a.xrows;
 }
 
-// bid -> tile of BT rows by outputs: consecutive workgroups go to different XCDs, so each XCD takes a
-// contiguous share of the tiles, in groups of up to 8 output tiles by all token tiles.  With experts the
-// shares are of the tiles that hold rows: of those that might, which are launched, the last ones hold none
-// (32768 rows of 64 experts by 4096 x 4096: 708 us with shares of all).
+// bid -> tile of BT rows by outputs (f8_place).  With experts the XCDs' shares are of the tiles that hold
+// rows: of those that might, which are launched, the last ones hold none (32768 rows of 64 experts by 4096 x
+// 4096, PWQ_E4M3_SUMS: 708 us with shares of all, 609 so).
 template <int BT>
 __device__ __forceinline__ bool f8_tile(const F8Args& a, uint32_t bid, int& to, F8Rows& r) {
     F8Count<BT> c;
     uint32_t tiles_t = (uint32_t)a.tiles_t;
     if (a.offsets) {
         tiles_t = 0;
-        for (int e0 = 0; e0 < a.experts; e0 += 64) tiles_t += (uint32_t)c.of(a, e0);
+        for (int e0 = 0; e0 < a.experts; e0 += 64) tiles_t = f8_upto(tiles_t, c.of(a, e0), a.tiles_t);
     }
-    const uint32_t nt = tiles_t * (uint32_t)a.tiles_m;    // below 2^24 (f8_plan_size_ok)
-    if (bid >= nt) return false;
-    const uint32_t x = bid & 7, per = nt >> 3, rem = nt & 7;
-    const uint32_t id = x * per + (x < rem ? x : rem) + (bid >> 3);
-    const uint32_t band = 8 * tiles_t, g = id / band, left = (uint32_t)a.tiles_m - 8 * g;
-    const uint32_t rows = left < 8 ? left : 8, in = id - g * band, down = in / rows;
-    const int tt = (int)down;
-    to = (int)(8 * g + in - down * rows);
-    if (a.offsets && a.experts <= 64) c.find(0, tt, r);
-    else r = f8_rows<BT>(a, tt);
+    const F8Place p = f8_place(bid, tiles_t, (uint32_t)a.tiles_m);
+    if (!p.there) return false;
+    to = p.to;
+    if (a.offsets && a.experts <= 64) c.find(0, p.tt, r);
+    else r = f8_rows<BT>(a, p.tt);
     return r.t0 < r.end;
 }
 
@@ -1122,8 +1115,9 @@ hipError_t f8_tile_go(F8Args a, bool e8, hipStream_t s) {
 }
 
 template <int U, int W>
-hipError_t f8_row_go(const F8Args& a, bool e8, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(a.m, 16), 1, (unsigned)f8_tiles_most(a.T, a.experts, 16));
+hipError_t f8_row_go(F8Args a, bool e8, hipStream_t s) {
+    a.tiles_t = (int)f8_tiles_most(a.T, a.experts, 16);
+    const dim3 grid((unsigned)cdiv(a.m, 16), 1, (unsigned)a.tiles_t);
     if (e8) hipLaunchKernelGGL((f8_row_kernel<U, W, true>), grid, dim3(64 * W), 0, s, a);
     else hipLaunchKernelGGL((f8_row_kernel<U, W, false>), grid, dim3(64 * W), 0, s, a);
     return hipGetLastError();

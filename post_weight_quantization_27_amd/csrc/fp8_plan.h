@@ -41,6 +41,37 @@ inline int64_t f8_tiles_most(int64_t T, int64_t experts, int64_t bt) {
     return T / bt + (T < experts ? T : experts);
 }
 
+// The kernels' side of the same (constexpr: device code too).  Offsets come from the device and may hold
+// anything: what is counted stays within the `most` tiles of BT rows that were launched, which offsets that
+// do not decrease never pass, so that 64 experts' tiles fit 31 bits and all tiles by outputs 24.
+//
+// an expert's rows lo .. hi - 1, taken into 0 .. T, in tiles of bt
+constexpr int64_t f8_low(int64_t lo) { return lo < 0 ? 0 : lo; }
+constexpr int64_t f8_high(int64_t hi, int64_t T) { return hi > T ? T : hi; }
+constexpr int f8_own(int64_t lo, int64_t hi, int bt, int most) {
+    const int64_t n = hi > lo ? (hi - lo + bt - 1) / bt : 0;
+    return n < most ? (int)n : most;
+}
+// tiles of the experts before, `have`, and of 64 more
+constexpr uint32_t f8_upto(uint32_t have, int more, int most) {
+    return have + (uint32_t)more < (uint32_t)most ? have + (uint32_t)more : (uint32_t)most;
+}
+// Workgroup bid of tiles_t by tiles_m tiles: consecutive workgroups go to different XCDs, so each XCD takes
+// a contiguous share of the tiles, in groups of up to 8 output tiles by all token tiles.
+struct F8Place {
+    int tt, to;                    // token tile, output tile
+    bool there;
+};
+constexpr F8Place f8_place(uint32_t bid, uint32_t tiles_t, uint32_t tiles_m) {
+    const uint32_t nt = tiles_t * tiles_m;
+    if (bid >= nt) return F8Place{0, 0, false};
+    const uint32_t x = bid & 7, per = nt >> 3, rem = nt & 7;
+    const uint32_t id = x * per + (x < rem ? x : rem) + (bid >> 3);
+    const uint32_t band = 8 * tiles_t, g = id / band, left = tiles_m - 8 * g;
+    const uint32_t rows = left < 8 ? left : 8, in = id - g * band, down = in / rows;
+    return F8Place{(int)down, (int)(8 * g + in - down * rows), true};
+}
+
 // What is expected of the experts' shares, which the host does not know: rows that choose any of them alike
 struct F8Shares {
     double active, rows;           // experts that have rows, and how many each
