@@ -115,3 +115,24 @@ def test_any_offsets_stay_inside_the_launch(tiles):
         assert counted <= most and sum64 < 2 ** 31
         assert 0 <= t0 and t1 < max(counted, 1) and 0 <= o0 and o1 < -(-m // bo)
         assert once
+
+
+def test_a_launch_has_every_share_of_rows(tiles):
+    """The launched tiles hold the rows however they are shared out: every expert one row past whole tiles,
+    fewer rows than experts, one expert with offsets, all rows at one expert."""
+    cases, want = [], []
+    for bt, bo in TILES:
+        for E in (1, 2, 3, 7, 64, 65, 200):
+            for q in (0, 1, 3):
+                shares = [[q * bt + 1] * E, [q * bt] * E, [q * bt + bt - 1] * E, [0] * (E - 1) + [q * bt * E + 1],
+                          [q * bt * E + E] + [0] * (E - 1), [q * bt + 1] + [1] * (E - 1), [i % 2 for i in range(E)]]
+                for counts in shares:
+                    if sum(counts):
+                        off = [0]
+                        for c in counts:
+                            off.append(off[-1] + c)
+                        cases.append((off[-1], 3 * bo, E, bt, bo, off))
+                        want.append(sum(-(-c // bt) for c in counts))
+    for w, (most, counted, *_, once) in zip(want, tiles(cases)):
+        assert w <= most and counted == w and once
+    assert any(w == most for w, (most, *_) in zip(want, tiles(cases)) if w > 1)       # and no fewer would do
