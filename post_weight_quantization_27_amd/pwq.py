@@ -500,10 +500,10 @@ def _pitch(t: torch.Tensor, name: str, dtypes, dev, shape=None) -> int:
     s0, s1 = t.stride()
     if s1 != 1 and sh[1] > 1:
         _bad(name, "contiguous columns")
-    if s0 < sh[1]:
-        if sh[0] > 1:
-            _bad(name, f"rows that do not overlap (stride {s0})")
+    if sh[0] <= 1:                  # one row's stride says nothing
         return sh[1]
+    if s0 < sh[1]:
+        _bad(name, f"rows that do not overlap (stride {s0})")
     return s0
 
 
