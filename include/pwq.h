@@ -542,14 +542,17 @@ pwq_status pwq_quantize_blocks_fp8(const void* W, int w_dtype, int64_t n_mats, i
  *             16 and there are rows enough, copies of X and of the codes (about as many bytes as they).
  * A block's sum over k, of exact products in float32, is multiplied by the product of its two scales,
  * formed in float32, and added to a float32 sum, which is rounded once to Y's type.
- * With PWQ_E4M3_SUMS the sums may come from the e4m3 matrix instruction, at up to twice the rate where there
- * are a few hundred tokens or more.  Of each eight consecutive products it keeps what is at least 2^-13 of the
+ * With PWQ_E4M3_SUMS the sums may come from the e4m3 matrix instruction, which takes half the time for prompts
+ * and hardly less for few tokens.  Of each eight consecutive products it keeps what is at least 2^-13 of the
  * largest: off by less than 2^-10 of the largest of each eight, with every scale multiplied in (1.5e-5 to 5e-5
  * of the result's norm on normal data, where a rounding to float16 is 2e-4; all of a result that is small
  * products beside large ones that cancel).  Scales that are powers of two then go into the instruction, which
  * adds a block to the float32 sum itself.  PWQ_EDTYPE with PWQ_F32.
  * Any alignment and sizes; rows of X and codes that start at multiples of 16 bytes take the faster
- * kernels, as do the copies of rows of other lengths.  Codes of NaN and scales of NaN give NaN.
+ * kernels, as do the copies of rows of other lengths.  Rows of a multiple of 16 bytes that start elsewhere (X or
+ * codes at another address, ldx no multiple of 16, or of 2^24 and more, or with rows[] n_x ldx of 2^32 and more)
+ * are not copied and take about twice as long: 2048 tokens by 8192 x 8192 233 us aligned, 477 with X and 530 with
+ * codes one byte on.  Codes of NaN and scales of NaN give NaN.
  *
  * pwq_quantized_matmul_fp8_grouped: the product of a layer of experts.  n_rows output rows are sorted
  * by expert: those of expert e are offsets[e] .. offsets[e + 1] - 1, any number of them.

@@ -262,8 +262,9 @@ __device__ __forceinline__ int f8_pos(int r, int c) { return c ^ ((r >> 1) & 7);
 // any byte and have any length.  Operands travel through registers into LDS, two steps ahead; LDS
 // has two buffers and a step one barrier.  The last step may be partial: each 16 bytes past the end
 // is the row's last 16 instead, moved down in registers, with 0 behind in both operands (a byte
-// from elsewhere may be NaN).  Loads at odd addresses bound it: 2000 rows by 8191 x d_in, bfloat16, 359 us
-// with d_in 8191, 280 with 8196 and 238 with 8192, and the tiles below 117.
+// from elsewhere may be NaN).  Loads at odd addresses and the conversions to float16 bound it: 2000 rows by
+// 8191 x d_in, bfloat16, 530 us with d_in 8191, 453 with 8196 and 440 with 8192, and the tiles below 234; with
+// PWQ_E4M3_SUMS 360, 281, 244 and 120.
 
 // The 16 bytes from byte `by` (0 .. 16) on, with 0 behind them
 __device__ __forceinline__ uint4 f8_drop(uint4 v, int by) {
@@ -457,19 +458,25 @@ __global__ __launch_bounds__(256) void f8_any_kernel(F8Args a) {
 //   KG = 2: each group takes every other stage for the whole tile (WO x 4 / WO waves), with stages of
 //           its own that its own waves copy; the two sums meet in LDS at the end.
 // NST stages: a stage's copies fly while the NST - 1 before it are used.  With two (256 x 256, whose
-// stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that the fragments
-// fit the registers, and each part of a stage is copied over as soon as it has been read (see the loop).
+// stages are 64 KB) the step is cut in two, each with its half of the wave's rows, so that half a step's
+// fragments are held at a time, and each part of a stage is copied over as soon as it has been read (see the
+// loop).
 //
-// Measured (kernel trace, operands cold, bfloat16 outputs): 8192 rows by 28672 x 8192 1410-1580 us with
-// float32 scales (2.4-2.7 PFLOP/s), 1290-1375 with powers of two (2.8-2.98), where the library's product
-// with one scale per tensor takes 1200-1330 on the same boards; float32 outputs 8192^3 862 us (1.27
-// PFLOP/s on the float16 instructions, whose library product reaches 1.48).  The clock falls to 1.75-2.0
-// GHz; a step of 256 x 256 takes 2340 cycles with powers of two and about 3000 with float32 scales, of 2048
-// that its instructions need.  Of a tile's time 1.7 us go before its first copy, 1.4 to 2 until that has
-// landed and 3 to 4 into the outputs (32 steps of 4096 inputs: 45).  Workgroups that go through several
-// tiles lose: the next tile's addresses cost registers (256 x 256 spills, 8192^3 5 %; 128 x 128, 300 rows
-// by 50304 x 768 45 us in place of 40), as does leaving out the instructions of waves without tokens
-// (1460 -> 1560).
+// Measured (kernel trace, operands cold, bfloat16 outputs): 8192^3 871-892 us (1.23-1.26 PFLOP/s on the
+// float16 instructions, whose library product reaches 1.48), 8192 rows by 28672 x 8192 3000-3160, in tiles of
+// 256 x 128: twice as many converted rows do not fit the registers.  With PWQ_E4M3_SUMS, in tiles of 256 x
+// 256, 8192^3 419-422 us and 8192 rows by 28672 x 8192 1455-1500 with float32 scales (2.6 PFLOP/s), 373-387
+// and 1325-1370 with powers of two (2.8-2.9), where the library's product with one scale per tensor takes
+// 1200-1330 on the same boards.  The clock falls to 1.6-2.0 GHz; a step of 256 x 256 takes 2340 cycles with
+// powers of two and about 3000 with float32 scales, of 2048 that its instructions need.  Of a tile's time 1.7
+// us go before its first copy, 1.4 to 2 until that has landed and 3 to 4 into the outputs (32 steps of 4096
+// inputs: 45).
+//
+// The kernels of 256 x 256 take all 256 registers and spill 11 to 39 more, in the set-up and the loops of the
+// last stages: 8192 rows by 28672 x 8192 write 595 MB with powers of two and 510 with float32 scales, for 470
+// of outputs.  Workgroups that go through several tiles, whose next addresses take registers too, lose (8192^3
+// 5 %, with more spilled; 128 x 128, 300 rows by 50304 x 768 45 us in place of 40), as does leaving out the
+// instructions of waves without tokens (1460 -> 1560).
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 __device__ const uint4 f8_zeros = {0u, 0u, 0u, 0u};
@@ -924,9 +931,11 @@ __device__ __forceinline__ void f8_tile_body(const F8Args& a, uint8_t* smem, int
     }
 }
 
-// HALF: a tile of 256 x 256 with no more than 128 rows, an expert's last, is one of 256 x 128 (16384 rows
-// of 64 experts by 4096 x 4096 396 -> 379 us, of 128 by 1024 x 2048 103 -> 90; 32768 of 64, at the power
-// limit, 622 -> 615).  One matrix has one such tile a column at most, and loses up to 1 % to it.
+// HALF: a tile of 256 x 256 with no more than 128 rows, an expert's last, is one of 256 x 128 (PWQ_E4M3_SUMS,
+// 16384 rows of 64 experts by 4096 x 4096 396 -> 379 us, of 128 by 1024 x 2048 103 -> 90; 32768 of 64, at the
+// power limit, 622 -> 615).  It starts at another k than the full tiles of the same weights, so more of them
+// comes from memory twice (32768 rows of 64 read 2447 MB in place of 1882).  One matrix has one such tile a
+// column at most, and loses up to 1 % to it.
 template <int BO, int BT, int NST, int WO, int KG, bool E8, bool EXACT, bool HALF>
 __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
     static_assert(!HALF || (BO == 256 && BT == 256), "half a tile");
@@ -952,7 +961,7 @@ __global__ __launch_bounds__(512) void f8_tile_kernel(F8Args a) {
 // The float16 instructions cost nothing here.  Loads past the rows or tokens take a 16-byte block of
 // zeros as their address, so none waits behind a branch.  1 row by 8192 x 8192 17 us (4.0 TB/s), by 768 x
 // 768 3.8 (an empty launch takes 2.2).  Rows of any alignment lose this way: 1 row by 28671 x 8191 108 us,
-// 57 with the 64 x 32 tiles above.
+// 58 with the 64 x 32 tiles above.
 template <int U, int W, bool E8>
 __global__ __launch_bounds__(64 * W) void f8_row_kernel(F8Args a) {
     __shared__ f32x4 red[W][64];

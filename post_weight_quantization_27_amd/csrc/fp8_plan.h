@@ -90,9 +90,10 @@ inline double f8_tiles_about(const F8Shares& e, int64_t T, int64_t experts, int6
 // Any alignment: the tile and the splits of k with the least estimate (us), rounds of tiles on 256
 // compute units, of which workgroups that share one overlap a part.  Fitted to the times over 210 shapes
 // with odd d_in (517 .. 14337 inputs, 769 .. 14337 outputs, 1 .. 3000 rows, one matrix and 7 or 32
-// experts, float32 and 16-bit outputs): 1.2 % longer than the fastest in the geometric mean and 24 % at the
-// worst; 64 x 64 tiles alone, unsplit, take 31 % longer in the mean.  333 rows by 5003 x 1601, float32
-// outputs: 19.7 us with 128 x 64, 22.8 with 64 x 64, 23.3 with 64 x 32; 16 by 4099 x 8191, bfloat16: 66, 45 and 30.
+// experts, float32 sums and the e4m3 instruction's): 1.2 % longer than the fastest in the geometric mean and
+// 24 % at the worst; 64 x 64 tiles alone, unsplit, take 31 % longer in the mean.  333 rows by 5003 x 1601: 19.4
+// us with 128 x 64, 21.9 with 64 x 64, 23.9 with 64 x 32; 16 by 4099 x 8191: 70, 52 and 35, with two splits of k
+// 40, 32 and 23.
 struct F8AnyCost {
     int bo, bt;
     float fixed, step, step_exact; // us per tile, and for each 128 k
@@ -144,12 +145,12 @@ constexpr int F8_TILES = sizeof(f8_tiles) / sizeof(f8_tiles[0]);
 
 // The least estimate (us) of: rounds of tiles on 256 compute units over 1 to 8 splits of k whose sums
 // a second launch joins, and no less than memory takes; or the row kernel, whose workgroups stream their 16
-// rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359
-// shapes (768 .. 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts, each output
-// and scale type): the choice takes 1.3 % longer than the fastest kernel in the geometric mean and 26 % at
-// the worst (256 rows of 8 experts by 2048 x 4096: 27.3 against 21.7 us), and over 70 drawn shapes with
-// float32 outputs 1.1 % and 24 %; 128 x 128 tiles alone take 58 % longer in the mean and up to 5.3 times as
-// long.
+// rows of codes once per 16 tokens.  The constants are fitted to the times of every kernel over 359 shapes,
+// before experts' tiles of 256 x 256 had a half form.  Over 544 shapes of the kernels as they are (768 ..
+// 28672 inputs and outputs, 1 .. 32768 rows, one matrix and 8 .. 128 experts) the choice takes 1.6 % longer than
+// the fastest kernel in the geometric mean and 36 % at the worst (1024 rows of 8 experts by 2048 x 4096: 49
+// against 36 us): of float32 sums 0.7 % for one matrix and 4.8 % for experts, of the e4m3 instruction's 1.1 %
+// (powers of two 1.8) and 3.4 %.  128 x 128 tiles alone take 59 % longer in the mean and up to 5.3 times as long.
 inline F8Plan f8_plan_fast(const F8Shape& s) {
     const F8Shares e = f8_shares(s.T, s.experts);
     const double bytes = ((double)s.T * s.n + e.active * (double)s.m * s.n + 2.0 * s.T * s.m) * 1e-6;      // MB
@@ -192,10 +193,11 @@ constexpr int64_t f8_laid(int64_t n) { return (n + 15) / 16 * 16; }
 
 // The kernel of a call.  Rows of any length are copied to rows of 16-byte multiples first where that and
 // the faster kernels are estimated to take less than the kernels for any alignment: a launch and the bytes
-// at 6 TB/s.  8000 rows by 8191 x 8191, bfloat16: 488 us with 42 of copies, 1367 without; 700 by 4099 x
-// 4111: 39 and 49; 128 by 4099 x 4111: 25 and 21.  Over 90 shapes with odd d_in (32 .. 10000 rows) the
-// choice takes 0.1 % longer than the better of the two in the mean and 6 % at the worst, no copies 11 %
-// and up to 2.5 times as long.
+// at 6 TB/s.  8000 rows by 8191 x 8191, bfloat16: 931 us with 42 of copies, 2096 without; 700 by 4111 x
+// 4099: 46 and 61; 333 by 5003 x 1601: 25 and 20.  With the e4m3 instruction's sums 496 and 1368, 38 and 49,
+// 23 and 17, and over 90 shapes with odd d_in (32 .. 10000 rows) the choice takes 0.1 % longer than the better
+// of the two in the mean and 6 % at the worst, no copies 11 % and up to 2.5 times as long.  A d_in that is a
+// multiple of 16 is not copied, wherever its rows start: every call's workspace would have to hold the copies.
 inline F8Plan f8_plan(const F8Shape& s) {
     if (s.fast) return f8_plan_fast(s);
     const F8Plan any = f8_plan_any(s);

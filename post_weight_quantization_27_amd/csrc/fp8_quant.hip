@@ -190,7 +190,9 @@ __global__ __launch_bounds__(256) void f8_tokens_kernel(F8QuantArgs a) {
 
 // ------------------------------------------------------------------ weights
 // A workgroup holds a block of 128 x 128, 64 values a thread.  Memory bounds it: 8192 x 28672 float16 141
-// us (5.0 TB/s), float32 217 (5.4); rows of odd length 8191 x 8191 bfloat16 58, where 8192 x 8192 takes 45.
+// us (5.0 TB/s), float32 217 (5.4); rows of odd length 8191 x 8191 bfloat16 58, where 8192 x 8192 takes 45: a
+// row of a block shares a line of 128 bytes with the next block, whose workgroup is on another XCD, and both
+// read it (201 MB for 134).
 template <int XT, int AL, bool E8>
 __global__ __launch_bounds__(256) void f8_blocks_kernel(F8QuantArgs a) {
     __shared__ float slot[2][4];

@@ -776,8 +776,8 @@ def quantized_matmul_fp8(X: torch.Tensor, x_scales: torch.Tensor, codes: torch.T
                          ws: Optional[torch.Tensor] = None, e4m3_sums: bool = False) -> torch.Tensor:
     """Y = X What^T on e4m3 codes with a scale per block of 128: X, x_scales from quantize_tokens_fp8,
     codes, scales from quantize_blocks_fp8 (both scales of one type).  Outputs are float32 sums of exact
-    products, rounded once.  ``e4m3_sums`` (16-bit outputs): sums may be the e4m3 matrix instruction's, at
-    up to twice the rate for prompts, off by up to 2^-10 of the largest product of each eight."""
+    products, rounded once.  ``e4m3_sums`` (16-bit outputs): sums may be the e4m3 matrix instruction's,
+    off by up to 2^-10 of the largest product of each eight, in half the time for prompts."""
     dev = X.device
     ldx, lds, st, c, sw = _fp8_operands(X, x_scales, codes, scales, dev, 2)
     T, d = X.shape
